@@ -494,6 +494,124 @@ MOE_API int moe_seq_balance_loss(const moe_config *cfg, int64_t T, int64_t seq_l
                                  const void *ws_dev, size_t ws_bytes, float *loss_dev, int32_t *err_flag_dev,
                                  void *stream);
 
+/* ------------------------------------------ norm in front of the layer */
+/* Residual addition, RMS norm and 1x128 quantization in one pass: what feeds
+ * the layer.  Per row of cols channels:
+ *   h = x + resid (rounded to dtype; h = x without resid)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)                        (FP32)
+ *   y = h * rstd * weight                                   (FP32)
+ *   y_dev: y rounded to bf16;  q_dev, scales_dev: the FP32 y quantized 1x128
+ *   (as fp8_quant_1x128, or as fp8_quant_1x128_pow2 with scale_mode
+ *   MOE_SCALE_POW2); a tile that holds an infinity or a NaN gets the scale
+ *   NaN and NaN codes.
+ *   x_dev, resid_dev  dtype [rows, ld_x] and [rows, ld_resid] (16-byte
+ *               aligned, ld >= cols and a multiple of 8); resid_dev nullable
+ *   dtype       MOE_DTYPE_BF16 or MOE_DTYPE_F32: x, resid and h
+ *   weight_dev  float [cols], 16-byte aligned, nullable (ones)
+ *   eps         > 0
+ *   h_dev       dtype [rows, cols], dense; required with resid_dev, else
+ *               nullable; may be x_dev or resid_dev (in place, when that one
+ *               is dense)
+ *   y_dev       bf16 [rows, cols], nullable
+ *   q_dev       E4M3 [rows, cols];  scales_dev float [rows, cols/128]
+ *   rstd_dev    float [rows], nullable (the backward reads it)
+ * rows >= 0 (0 enqueues nothing), cols % 128 == 0, cols <= 32768. */
+MOE_API int fp8_add_rmsnorm_quant_1x128(const void *x_dev, int64_t ld_x, const void *resid_dev, int64_t ld_resid,
+                                        int32_t dtype, const float *weight_dev, float eps, int64_t rows, int64_t cols,
+                                        void *h_dev, void *y_dev, uint8_t *q_dev, float *scales_dev, float *rstd_dev,
+                                        int32_t scale_mode, void *stream);
+
+/* Its backward (the quantization passes the gradient through), with
+ * n = h * rstd and g = dy * weight, in FP32:
+ *   dx = dres + rstd * (g - n * mean(g * n))    (the gradient of x and of resid)
+ *   dweight[c] = sum over rows of dy * n        (overwritten; rows in a fixed
+ *                order, so every run gives the same bits)
+ *   dy_dev    dy_dtype [rows, cols]: gradient of y
+ *   h_dev     dtype [rows, cols];  rstd_dev float [rows]: the forward's
+ *   dres_dev  dtype [rows, cols], nullable (0): gradient that reaches h past
+ *             the norm
+ *   dx_dev    dx_dtype [rows, cols]; may be dy_dev, h_dev or dres_dev when its
+ *             type is the same
+ *   dweight_dev float [cols], nullable
+ *   ws_dev    add_rmsnorm_backward_workspace_size() bytes, 256-byte aligned
+ *             (only with dweight_dev)
+ * rows == 0 writes zeros to dweight_dev. */
+MOE_API size_t add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+MOE_API int add_rmsnorm_backward(const void *dy_dev, int32_t dy_dtype, const void *h_dev, const void *dres_dev,
+                                 int32_t dtype, const float *weight_dev, const float *rstd_dev, int64_t rows,
+                                 int64_t cols, void *dx_dev, int32_t dx_dtype, float *dweight_dev, void *ws_dev,
+                                 size_t ws_bytes, void *stream);
+
+/* ------------------------------------- balance loss of packed sequences */
+/* K splits of the router's logit partials that moe_route leaves at the start
+ * of its workspace and moe_forward at moe_ws_layout.logits: float [n_splits,
+ * T, N_r], their sum over the splits being the logits.  (The number follows
+ * the current device's SM count.)  A negative status for an invalid cfg or T. */
+MOE_API int moe_router_splits(const moe_config *cfg, int64_t T);
+
+/* Sequence-wise balance loss and per-expert counts of a batch of packed
+ * sequences of any lengths (moe_seq_balance_loss takes equal ones and gives
+ * the loss alone).  Sequence s holds the tokens [seq_offsets[s],
+ * seq_offsets[s + 1]), L of them:
+ *   counts[s, i] = picks of expert i,  f_i = N_r / (K_r L) * counts[s, i]
+ *   loss[s] = alpha * sum_i f_i * (1/L) sum_t s_{i,t} / sum_j s_{j,t}
+ * An empty sequence has loss 0 and counts 0; tokens before the first offset
+ * or from the last one on belong to no sequence.
+ *   logits_dev  float [n_splits, T, N_r], 16-byte aligned (moe_router_splits,
+ *               or 1 for logits of the caller's own)
+ *   idx_dev     int32 [T, K_r]
+ *   seq_offsets_dev int32 [n_seq + 1], ascending, in [0, T]
+ *   loss_dev    float [n_seq];  counts_dev int32 [n_seq, N_r]
+ *   ws_dev      moe_balance_loss_workspace_size() bytes, 256-byte aligned
+ *   err_flag_dev gets MOE_DEVERR_BAD_INDEX for an expert index out of range
+ *               (not counted) and for offsets that are not as above (such a
+ *               sequence is read as empty)
+ * n_seq == 0 enqueues nothing.  The additions' order is fixed: every run gives
+ * the same bits. */
+MOE_API size_t moe_balance_loss_workspace_size(const moe_config *cfg, int64_t T, int64_t n_seq);
+MOE_API int moe_balance_loss(const moe_config *cfg, const float *logits_dev, int32_t n_splits, const int32_t *idx_dev,
+                             int64_t T, const int32_t *seq_offsets_dev, int64_t n_seq, float alpha, float *loss_dev,
+                             int32_t *counts_dev, void *ws_dev, size_t ws_bytes, int32_t *err_flag_dev, void *stream);
+
+/* ------------------------------------------------------ router backward */
+/* Gradient of the balance loss: seq_offsets, n_seq, alpha as given to
+ * moe_balance_loss and counts as it wrote them (constants of the gradient);
+ * dloss float [n_seq], nullable (ones): the gradient of each loss. */
+typedef struct {
+    const int32_t *seq_offsets_dev;
+    int32_t n_seq;
+    float alpha;
+    const int32_t *counts_dev;
+    const float *dloss_dev;
+} moe_balance_grad;
+
+/* Backward of the router, the choice of experts held fixed: the gradient of
+ * the logits z = x . e_i from the gradients of the gates and of the balance
+ * loss, and its two products.  With gh_k = s_k / sum_sel s of the chosen
+ * experts and p_i = s_i / sum_j s_j:
+ *   dz_k += (1 - s_k) gh_k (r_k - sum_j r_j gh_j),  r_k = route_scale dgate_k
+ *   dz_i += dloss alpha / L  p_i (1 - s_i) (f_i - sum_j f_j p_j)
+ *   dx = dz W_r,  dW_r = dz^T x
+ * dz is FP32; the products keep its 24 bits (three bf16 parts on the tensor
+ * cores, FP32 accumulation) and give the same bits on every run.
+ *   logits_dev, n_splits, idx_dev  as in moe_balance_loss
+ *   dgate_dev   float [T, K_r], nullable: gradient of the gates
+ *   balance     nullable
+ *   x_dev       bf16 [T, H] (for dwr_dev);  wr_dev bf16 [N_r, H] (for dx_dev)
+ *   dlogits_dev float [T, N_r], nullable: dz
+ *   dx_dev      float [T, H], nullable; dx_accumulate != 0 adds to it (e.g. to
+ *               moe_backward's dx), else it is overwritten
+ *   dwr_dev     float [N_r, H], nullable (T == 0 writes zeros)
+ *   ws_dev      moe_router_backward_workspace_size() bytes, 256-byte aligned
+ *               (only with dx_dev or dwr_dev)
+ *   err_flag_dev as in moe_balance_loss */
+MOE_API size_t moe_router_backward_workspace_size(const moe_config *cfg, int64_t T);
+MOE_API int moe_router_backward(const moe_config *cfg, const float *logits_dev, int32_t n_splits,
+                                const int32_t *idx_dev, int64_t T, const float *dgate_dev,
+                                const moe_balance_grad *balance, const void *x_dev, const void *wr_dev,
+                                float *dlogits_dev, float *dx_dev, int32_t dx_accumulate, float *dwr_dev, void *ws_dev,
+                                size_t ws_bytes, int32_t *err_flag_dev, void *stream);
+
 /* ------------------------------------------------------------ errors */
 /* Synchronises `stream`, copies *err_flag_dev to *host_value (nullable) and
  * returns MOE_OK if it is 0, MOE_ERR_TIMEOUT if the timeout bit is set, else

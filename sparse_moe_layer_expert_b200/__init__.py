@@ -18,5 +18,7 @@ from ._binding import (  # noqa: F401
     MOE_GEMM_SINGLE, MOE_GEMM_BLOCK_SCALED, MOE_GEMM_TALL,
     moe_workspace_size, new_err_flag, weights_struct, ws_view, moe_ep_row_bytes, moe_ep_dispatch, moe_ep_experts,
     moe_ep_combine, moe_transpose_weights, moe_backward, moe_backward_workspace_layout,
+    fp8_add_rmsnorm_quant_1x128, add_rmsnorm_backward, moe_router_splits, moe_route_logits, moe_balance_loss,
+    moe_router_backward,
 )
 from .layer import MoeLayer  # noqa: F401

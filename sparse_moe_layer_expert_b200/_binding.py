@@ -45,7 +45,9 @@ EXPORTS = (
     "moe_route_noalloc", "moe_seq_balance_loss", "moe_set_gemm_variant", "moe_gemm_kernel_for",
     "moe_ep_row_bytes", "moe_ep_dispatch_workspace_size", "moe_ep_dispatch", "moe_ep_experts_workspace_size",
     "moe_ep_experts", "moe_ep_combine", "moe_transpose_weights", "moe_backward_workspace_size", "moe_backward",
-    "moe_backward_workspace_layout",
+    "moe_backward_workspace_layout", "fp8_add_rmsnorm_quant_1x128", "add_rmsnorm_backward_workspace_size",
+    "add_rmsnorm_backward", "moe_router_splits", "moe_balance_loss_workspace_size", "moe_balance_loss",
+    "moe_router_backward_workspace_size", "moe_router_backward",
 )
 MOE_GEMM_AUTO = 0
 MOE_GEMM_SINGLE = 1
@@ -125,10 +127,29 @@ lib.moe_backward_workspace_size.restype = _sz
 lib.moe_backward_workspace_size.argtypes = [_cfgp, _i64]
 lib.moe_backward.argtypes = [_cfgp, C.POINTER(MoeWeights), _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
                              _sz, _vp, _sz, _vp, _vp]
+class MoeBalanceGrad(C.Structure):
+    _fields_ = [("seq_offsets_dev", C.c_void_p), ("n_seq", C.c_int32), ("alpha", C.c_float),
+                ("counts_dev", C.c_void_p), ("dloss_dev", C.c_void_p)]
+
+
+lib.fp8_add_rmsnorm_quant_1x128.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                                            _i32, _vp]
+lib.add_rmsnorm_backward_workspace_size.restype = _sz
+lib.add_rmsnorm_backward_workspace_size.argtypes = [_i64, _i64]
+lib.add_rmsnorm_backward.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _i32, _vp, _vp, _sz, _vp]
+lib.moe_router_splits.argtypes = [_cfgp, _i64]
+lib.moe_balance_loss_workspace_size.restype = _sz
+lib.moe_balance_loss_workspace_size.argtypes = [_cfgp, _i64, _i64]
+lib.moe_balance_loss.argtypes = [_cfgp, _vp, _i32, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp, _vp]
+lib.moe_router_backward_workspace_size.restype = _sz
+lib.moe_router_backward_workspace_size.argtypes = [_cfgp, _i64]
+lib.moe_router_backward.argtypes = [_cfgp, _vp, _i32, _vp, _i64, _vp, C.POINTER(MoeBalanceGrad), _vp, _vp, _vp, _vp,
+                                    _i32, _vp, _vp, _sz, _vp, _vp]
 for _name in EXPORTS:
     if _name not in ("moe_status_string", "moe_route_workspace_size", "moe_workspace_size", "moe_ep_row_bytes",
                      "moe_ep_dispatch_workspace_size", "moe_ep_experts_workspace_size",
-                     "moe_backward_workspace_size"):
+                     "moe_backward_workspace_size", "add_rmsnorm_backward_workspace_size",
+                     "moe_balance_loss_workspace_size", "moe_router_backward_workspace_size"):
         getattr(lib, _name).restype = C.c_int
 
 
@@ -397,6 +418,225 @@ def moe_backward(cfg: MoeConfig, w: dict, wt: dict, x, dout, fwd_ws, dx=None, dW
                             _ptr(wt["s2t"]), _ptr(x), _ptr(dout), T, _ptr(dx), _ptr(dW13), _ptr(dW2), _ptr(fwd_ws),
                             fwd_ws.numel(), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "moe_backward")
     return dx, dW13, dW2
+
+
+# ------------------------------------------- norm, balance loss, router
+def _want(where: str, t, name: str, dtype, shape, device=None, contiguous=True) -> None:
+    """Raise MoeError(MOE_ERR_INVALID_ARG) unless t is a tensor of that type
+    and shape (None: any) on that CUDA device."""
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda
+            or (device is not None and t.device != device) or (shape is not None and t.shape != shape)
+            or (contiguous and not t.is_contiguous())):
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is {got}, wanted "
+                       f"{'/'.join(str(d) for d in dtypes)}{'' if shape is None else ' ' + str(tuple(shape))}"
+                       f"{' contiguous' if contiguous else ''} on {device or 'a CUDA device'}")
+
+
+class _on:
+    """Make `device` current for a call (the library launches on the current
+    device) and give the call's stream: the caller's, or that device's
+    current one."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guard = device, stream, None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_STREAM_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _code(dtype) -> int:
+    return MOE_DTYPE_F32 if dtype == torch.float32 else MOE_DTYPE_BF16
+
+
+def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: float = 1e-6, h=None, y=None, q=None,
+                                scales=None, rstd=None, pow2: bool = False, stream=None):
+    """h = x + resid, y = h / rms(h) * weight, and y quantized 1x128, in one
+    pass.  x, resid: bf16 or float32 [rows, cols] (rows may be strided);
+    weight: float32 [cols] or None.  Returns (h, y bf16, q uint8, scales,
+    rstd); without resid, h is x unless a buffer is given."""
+    where = "fp8_add_rmsnorm_quant_1x128"
+    _want(where, x, "x", _STREAM_TYPES, None, contiguous=False)
+    if x.dim() != 2 or (x.numel() and x.stride(1) != 1):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: x is [rows, cols] with unit stride along cols")
+    dev, shape = x.device, x.shape
+    rows, cols = shape
+    if resid is not None:
+        _want(where, resid, "resid", x.dtype, shape, dev, contiguous=False)
+        if resid.numel() and resid.stride(1) != 1:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: resid has unit stride along cols")
+        h = torch.empty(shape, dtype=x.dtype, device=dev) if h is None else h
+    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if y is None else y
+    q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
+    sshape = (rows, cols // 128)
+    scales = torch.empty(sshape, dtype=torch.float32, device=dev) if scales is None else scales
+    rstd = torch.empty((rows,), dtype=torch.float32, device=dev) if rstd is None else rstd
+    if weight is not None:
+        _want(where, weight, "weight", torch.float32, (cols,), dev)
+    if h is not None:
+        _want(where, h, "h", x.dtype, shape, dev)
+    _want(where, y, "y", torch.bfloat16, shape, dev)
+    _want(where, q, "q", torch.uint8, shape, dev)
+    _want(where, scales, "scales", torch.float32, sshape, dev)
+    _want(where, rstd, "rstd", torch.float32, (rows,), dev)
+    # a single row has no row stride
+    ld = x.stride(0) if rows > 1 else cols
+    ldr = cols if resid is None or rows <= 1 else resid.stride(0)
+    with _on(dev, stream) as st:
+        _check(lib.fp8_add_rmsnorm_quant_1x128(_ptr(x), ld, _ptr(resid), ldr, _code(x.dtype), _ptr(weight), eps, rows,
+                                               cols, _ptr(h), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd),
+                                               MOE_SCALE_POW2 if pow2 else MOE_SCALE_AMAX, st), where)
+    return x if h is None else h, y, q, scales, rstd
+
+
+def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, dx_dtype=None, ws=None, stream=None):
+    """Gradients of fp8_add_rmsnorm_quant_1x128 (straight through the
+    quantization): (dx, dweight).  dy: gradient of y (bf16 or float32); h,
+    rstd: the forward's; dres: gradient reaching h past the norm, of h's type.
+    dx (the gradient of x and of resid) has dx_dtype, by default h's type."""
+    where = "add_rmsnorm_backward"
+    _want(where, h, "h", _STREAM_TYPES, None)
+    if h.dim() != 2:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: h is [rows, cols]")
+    dev, shape = h.device, h.shape
+    rows, cols = shape
+    _want(where, dy, "dy", _STREAM_TYPES, shape, dev)
+    _want(where, rstd, "rstd", torch.float32, (rows,), dev)
+    if weight is not None:
+        _want(where, weight, "weight", torch.float32, (cols,), dev)
+    if dres is not None:
+        _want(where, dres, "dres", h.dtype, shape, dev)
+    dx = torch.empty(shape, dtype=dx_dtype or h.dtype, device=dev) if dx is None else dx
+    _want(where, dx, "dx", _STREAM_TYPES if dx_dtype is None else dx_dtype, shape, dev)
+    dw = torch.empty((cols,), dtype=torch.float32, device=dev) if dw is None else dw
+    _want(where, dw, "dw", torch.float32, (cols,), dev)
+    with _on(dev, stream) as st:
+        if ws is None:
+            ws = torch.empty(max(int(lib.add_rmsnorm_backward_workspace_size(rows, cols)), 256), dtype=torch.uint8,
+                             device=dev)
+        _want(where, ws, "ws", torch.uint8, None, dev)
+        _check(lib.add_rmsnorm_backward(_ptr(dy), _code(dy.dtype), _ptr(h), _ptr(dres), _code(h.dtype), _ptr(weight),
+                                        _ptr(rstd), rows, cols, _ptr(dx), _code(dx.dtype), _ptr(dw), _ptr(ws),
+                                        ws.numel(), st), where)
+    return dx, dw
+
+
+def moe_router_splits(cfg: MoeConfig, T: int) -> int:
+    """K splits of the router's logit partials on the current device."""
+    r = lib.moe_router_splits(C.byref(cfg), int(T))
+    if r < 0:
+        _check(r, "moe_router_splits")
+    return r
+
+
+def moe_route_logits(cfg: MoeConfig, T: int, ws: torch.Tensor) -> torch.Tensor:
+    """The logit partials [n_splits, T, N_r] that moe_route left in its
+    workspace (a view; their sum over the splits is the logits)."""
+    n = moe_router_splits(cfg, T)
+    return ws[:n * T * cfg.n_routed * 4].view(torch.float32).view(n, T, cfg.n_routed)
+
+
+def _router_state(where: str, cfg: MoeConfig, logits, idx):
+    _want(where, logits, "logits", torch.float32, None)
+    if logits.dim() != 3 or logits.shape[0] < 1 or logits.shape[2] != cfg.n_routed:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: logits is [n_splits, T, {cfg.n_routed}]")
+    n, T, _ = logits.shape
+    _want(where, idx, "idx", torch.int32, (T, cfg.top_k), logits.device)
+    return n, T, logits.device
+
+
+def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e-4, loss=None, counts=None, ws=None,
+                     err=None, stream=None):
+    """Sequence-wise balance loss and per-expert counts of packed sequences:
+    (loss [n_seq], counts int32 [n_seq, N_r]).  logits: float32 [n_splits, T,
+    N_r] (moe_route_logits, or the caller's own with n_splits = 1); idx: the
+    picks; seq_offsets: int32 [n_seq + 1]."""
+    where = "moe_balance_loss"
+    n, T, dev = _router_state(where, cfg, logits, idx)
+    _want(where, seq_offsets, "seq_offsets", torch.int32, None, dev)
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: seq_offsets is [n_seq + 1]")
+    n_seq = seq_offsets.numel() - 1
+    loss = torch.empty((n_seq,), dtype=torch.float32, device=dev) if loss is None else loss
+    counts = torch.empty((n_seq, cfg.n_routed), dtype=torch.int32, device=dev) if counts is None else counts
+    _want(where, loss, "loss", torch.float32, (n_seq,), dev)
+    _want(where, counts, "counts", torch.int32, (n_seq, cfg.n_routed), dev)
+    with _on(dev, stream) as st:
+        if ws is None:
+            ws = torch.empty(max(int(lib.moe_balance_loss_workspace_size(C.byref(cfg), T, n_seq)), 256),
+                             dtype=torch.uint8, device=dev)
+        _want(where, ws, "ws", torch.uint8, None, dev)
+        err = new_err_flag(dev) if err is None else err
+        _want(where, err, "err", torch.int32, None, dev)
+        _check(lib.moe_balance_loss(C.byref(cfg), _ptr(logits), n, _ptr(idx), T, _ptr(seq_offsets), n_seq, alpha,
+                                    _ptr(loss), _ptr(counts), _ptr(ws), ws.numel(), _ptr(err), st), where)
+    return loss, counts
+
+
+def _balance_struct(where: str, cfg: MoeConfig, b: dict, dev) -> MoeBalanceGrad:
+    off, counts, dloss = b["seq_offsets"], b["counts"], b.get("dloss")
+    _want(where, off, "seq_offsets", torch.int32, None, dev)
+    if off.dim() != 1 or off.numel() < 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: seq_offsets is [n_seq + 1]")
+    n_seq = off.numel() - 1
+    _want(where, counts, "counts", torch.int32, (n_seq, cfg.n_routed), dev)
+    if dloss is not None:
+        _want(where, dloss, "dloss", torch.float32, (n_seq,), dev)
+    return MoeBalanceGrad(_ptr(off), n_seq, b.get("alpha", 1e-4), _ptr(counts), _ptr(dloss))
+
+
+def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None, balance=None, dlogits=None, dx=None,
+                        dx_accumulate: bool = False, dwr=None, ws=None, err=None, stream=None):
+    """Backward of the router with the picks held fixed: (dlogits, dx, dwr),
+    each only where asked for (True allocates it, a tensor is written, None
+    leaves it out).
+    dgate: gradient of the gates, float32 [T, K_r]; balance: dict(seq_offsets,
+    counts, dloss (None: ones), alpha) of the balance loss; x bf16 [T, H] for
+    dwr, wr bf16 [N_r, H] for dx.  dx_accumulate adds to dx."""
+    where = "moe_router_backward"
+    n, T, dev = _router_state(where, cfg, logits, idx)
+    H, Nr = cfg.hidden, cfg.n_routed
+
+    def out(t, name, shape):
+        if t is None or t is False:
+            return None
+        t = torch.empty(shape, dtype=torch.float32, device=dev) if t is True else t
+        _want(where, t, name, torch.float32, shape, dev)
+        return t
+
+    if dx_accumulate and not isinstance(dx, torch.Tensor):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: dx_accumulate needs a dx to add to")
+    dlogits, dx, dwr = out(dlogits, "dlogits", (T, Nr)), out(dx, "dx", (T, H)), out(dwr, "dwr", (Nr, H))
+    if dgate is not None:
+        _want(where, dgate, "dgate", torch.float32, (T, cfg.top_k), dev)
+    if x is not None or dwr is not None:
+        _want(where, x, "x", torch.bfloat16, (T, H), dev)
+    if wr is not None or dx is not None:
+        _want(where, wr, "wr", torch.bfloat16, (Nr, H), dev)
+    bal = None if balance is None else C.byref(_balance_struct(where, cfg, balance, dev))
+    with _on(dev, stream) as st:
+        if ws is None and (dx is not None or dwr is not None):
+            ws = torch.empty(max(int(lib.moe_router_backward_workspace_size(C.byref(cfg), T)), 256),
+                             dtype=torch.uint8, device=dev)
+        if ws is not None:
+            _want(where, ws, "ws", torch.uint8, None, dev)
+        err = new_err_flag(dev) if err is None else err
+        _want(where, err, "err", torch.int32, None, dev)
+        _check(lib.moe_router_backward(C.byref(cfg), _ptr(logits), n, _ptr(idx), T, _ptr(dgate), bal, _ptr(x), _ptr(wr),
+                                       _ptr(dlogits), _ptr(dx), int(dx_accumulate), _ptr(dwr), _ptr(ws),
+                                       0 if ws is None else ws.numel(), _ptr(err), st), where)
+    return dlogits, dx, dwr
 
 
 def ws_view(ws: torch.Tensor, layout: dict, name: str, dtype, shape) -> torch.Tensor:

@@ -1071,6 +1071,180 @@ int moe_seq_balance_loss(const moe_config *cfg, int64_t T, int64_t seq_len, floa
                                              err_flag, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------- around the layer: norm, router
+namespace {
+inline bool dtype_ok(int32_t d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+constexpr int64_t kMaxSeqs = kMaxTokens;
+constexpr int32_t kMaxSplits = 1024;
+
+int check_balance(const moe_balance_grad *b) {
+  if (b->n_seq < 0 || b->n_seq > kMaxSeqs || !(b->alpha == b->alpha)) return MOE_ERR_INVALID_ARG;
+  if (!b->seq_offsets_dev || (b->n_seq > 0 && !b->counts_dev)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(b->seq_offsets_dev) || !aligned4(b->counts_dev) || !aligned4(b->dloss_dev)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+struct RouterBwdLayout {
+  size_t parts[2], dwr[2], total;
+};
+void make_router_bwd_layout(const moe_config *c, int64_t T, RouterBwdLayout *L) {
+  Carve cv;
+  cv.take(L->parts, static_cast<size_t>(3) * T * moe::router_parts_pitch(c->n_routed) * 2);
+  const int64_t split = moe::router_dwr_split(T, c->hidden);
+  cv.take(L->dwr, split > 1 ? static_cast<size_t>(split) * moe::router_dwr_rows(c->n_routed) * c->hidden * 4 : 0);
+  L->total = (cv.off + 255) & ~size_t(255);
+}
+
+// The launches of the router's backward; g carries everything but the parts.
+cudaError_t run_router_bwd(const moe_config *cfg, moe::RouterBwd g, const void *x, const void *wr, float *dx,
+                           int accumulate, float *dwr, void *ws, cudaStream_t st) {
+  RouterBwdLayout L;
+  make_router_bwd_layout(cfg, g.T, &L);
+  g.parts = dx || dwr ? at<void *>(ws, L.parts) : nullptr;
+  cudaError_t e = moe::launch_router_dz(g, st);
+  if (e == cudaSuccess && dx)
+    e = moe::launch_router_dx(g.parts, wr, g.T, g.Nr, cfg->hidden, dx, accumulate, g.err, moe::kDefaultWaitLimitNs, st);
+  if (e == cudaSuccess && dwr)
+    e = moe::launch_router_dwr(g.parts, x, g.T, g.Nr, cfg->hidden, at<float *>(ws, L.dwr), dwr, g.err,
+                               moe::kDefaultWaitLimitNs, st);
+  return e;
+}
+}  // namespace
+
+int fp8_add_rmsnorm_quant_1x128(const void *x, int64_t ld_x, const void *resid, int64_t ld_resid, int32_t dtype,
+                                const float *weight, float eps, int64_t rows, int64_t cols, void *h, void *y,
+                                uint8_t *q, float *scales, float *rstd, int32_t scale_mode, void *stream) {
+  const NvtxRange nvtx_call("fp8_add_rmsnorm_quant_1x128");
+  if (rows < 0 || cols <= 0 || ld_x < cols || (ld_x % 8) != 0 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  if (resid && (ld_resid < cols || (ld_resid % 8) != 0 || !h)) return MOE_ERR_INVALID_ARG;
+  if (scale_mode != MOE_SCALE_AMAX && scale_mode != MOE_SCALE_POW2) return MOE_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  if (cols % 128 || cols > kMaxK || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(resid) || !aligned16(weight) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
+      !aligned4(scales) || !aligned4(rstd))
+    return MOE_ERR_INVALID_ARG;
+  // h may take x's or resid's place, row for row
+  if (h && ((h == x && ld_x != cols) || (h == resid && ld_resid != cols))) return MOE_ERR_INVALID_ARG;
+  if (const int d = check_device()) return d;
+  return cuda_status(moe::launch_add_rmsnorm_quant(x, ld_x, resid, ld_resid, dtype == MOE_DTYPE_F32, weight, eps, rows,
+                                                   static_cast<int>(cols), h, y, q, scales, rstd,
+                                                   scale_mode == MOE_SCALE_POW2, static_cast<cudaStream_t>(stream)));
+}
+
+size_t add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > INT32_MAX || cols <= 0 || cols % 128 || cols > kMaxK) return 0;
+  const size_t n = static_cast<size_t>(moe::norm_bwd_parts(rows, static_cast<int>(cols))) * cols * 4;
+  return n < 256 ? 256 : n;
+}
+
+int add_rmsnorm_backward(const void *dy, int32_t dy_dtype, const void *h, const void *dres, int32_t dtype,
+                         const float *weight, const float *rstd, int64_t rows, int64_t cols, void *dx,
+                         int32_t dx_dtype, float *dw, void *ws, size_t ws_bytes, void *stream) {
+  const NvtxRange nvtx_call("add_rmsnorm_backward");
+  if (rows < 0 || cols <= 0 || !dtype_ok(dy_dtype) || !dtype_ok(dtype) || !dtype_ok(dx_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (cols % 128 || cols > kMaxK || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(dres) || !aligned16(weight) || !aligned16(dx) || !aligned4(rstd) ||
+      !aligned4(dw) || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if (!dy || !h || !rstd || !dx || (dw && !ws)) return MOE_ERR_INVALID_ARG;
+    // dx may take the place of an input whose elements are as wide
+    if ((dx == dy && dx_dtype != dy_dtype) || ((dx == h || dx == dres) && dx_dtype != dtype)) return MOE_ERR_INVALID_ARG;
+    if (dw && ws_bytes < add_rmsnorm_backward_workspace_size(rows, cols)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  } else if (!dw) {
+    return MOE_OK;
+  }
+  if (const int d = check_device()) return d;
+  return cuda_status(moe::launch_add_rmsnorm_bwd(dy, dy_dtype == MOE_DTYPE_F32, h, dres, dtype == MOE_DTYPE_F32, weight,
+                                                 rstd, rows, static_cast<int>(cols), dx, dx_dtype == MOE_DTYPE_F32, dw,
+                                                 static_cast<float *>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int moe_router_splits(const moe_config *cfg, int64_t T) {
+  if (const int c = check_cfg(cfg)) return c;
+  if (T < 0 || T > kMaxTokens) return MOE_ERR_INVALID_ARG;
+  return moe::router_ksplit(T, cfg->n_routed, cfg->hidden);
+}
+
+size_t moe_balance_loss_workspace_size(const moe_config *cfg, int64_t T, int64_t n_seq) {
+  if (check_cfg(cfg) != MOE_OK || T < 0 || T > kMaxTokens || n_seq < 0 || n_seq > kMaxSeqs) return 0;
+  const size_t n = static_cast<size_t>(moe::balance_pieces(T, n_seq)) * cfg->n_routed * 8;
+  return n < 256 ? 256 : n;
+}
+
+int moe_balance_loss(const moe_config *cfg, const float *logits, int32_t n_splits, const int32_t *idx, int64_t T,
+                     const int32_t *seq_offsets, int64_t n_seq, float alpha, float *loss, int32_t *counts, void *ws,
+                     size_t ws_bytes, int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_balance_loss");
+  if (const int c = check_cfg(cfg)) return c;
+  if (T < 0 || T > kMaxTokens || n_seq < 0 || n_seq > kMaxSeqs || n_splits < 1 || n_splits > kMaxSplits ||
+      !(alpha == alpha))
+    return MOE_ERR_INVALID_ARG;
+  if (n_seq == 0) return MOE_OK;
+  if (!seq_offsets || !loss || !counts || !ws || !err_flag || (T > 0 && (!logits || !idx))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(idx) || !aligned4(seq_offsets) || !aligned4(loss) || !aligned4(counts) ||
+      !aligned4(err_flag) || (reinterpret_cast<uintptr_t>(ws) & 255))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_balance_loss_workspace_size(cfg, T, n_seq)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int d = check_device()) return d;
+  auto *p = static_cast<float *>(ws);
+  const int64_t pieces = moe::balance_pieces(T, n_seq);
+  return cuda_status(moe::launch_balance_loss(logits, n_splits, T, cfg->n_routed, cfg->top_k, idx, seq_offsets,
+                                              static_cast<int>(n_seq), alpha, p,
+                                              reinterpret_cast<int32_t *>(p + pieces * cfg->n_routed), loss, counts,
+                                              err_flag, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_router_backward_workspace_size(const moe_config *cfg, int64_t T) {
+  if (check_cfg(cfg) != MOE_OK || T < 0 || T > kMaxTokens) return 0;
+  RouterBwdLayout L;
+  make_router_bwd_layout(cfg, T, &L);
+  return L.total < 256 ? 256 : L.total;
+}
+
+int moe_router_backward(const moe_config *cfg, const float *logits, int32_t n_splits, const int32_t *idx, int64_t T,
+                        const float *dgate, const moe_balance_grad *balance, const void *x, const void *wr,
+                        float *dlogits, float *dx, int32_t dx_accumulate, float *dwr, void *ws, size_t ws_bytes,
+                        int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_router_backward");
+  if (const int c = check_cfg(cfg)) return c;
+  if (T < 0 || T > kMaxTokens || n_splits < 1 || n_splits > kMaxSplits) return MOE_ERR_INVALID_ARG;
+  if (balance)
+    if (const int c = check_balance(balance)) return c;
+  if (!err_flag || (dx && !wr) || (dwr && T > 0 && !x)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !idx || ((dx || dwr) && !ws))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(idx) || !aligned4(dgate) || !aligned16(x) || !aligned16(wr) ||
+      !aligned4(dlogits) || !aligned16(dx) || !aligned16(dwr) || !aligned4(err_flag) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0 && !dwr) return MOE_OK;
+  if (T > 0 && (dx || dwr) && ws_bytes < moe_router_backward_workspace_size(cfg, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int d = check_device()) return d;
+  moe::RouterBwd g{};
+  g.partial = logits;
+  g.n_ks = n_splits;
+  g.T = T;
+  g.Nr = cfg->n_routed;
+  g.Kr = cfg->top_k;
+  g.route_scale = cfg->route_scale;
+  g.idx = idx;
+  g.dgate = dgate;
+  if (balance && balance->n_seq > 0) {
+    g.off = balance->seq_offsets_dev;
+    g.n_seq = balance->n_seq;
+    g.counts = balance->counts_dev;
+    g.dloss = balance->dloss_dev;
+    g.alpha = balance->alpha;
+  }
+  g.dlogits = dlogits;
+  g.err = err_flag;
+  return cuda_status(
+      run_router_bwd(cfg, g, x, wr, dx, dx_accumulate, dwr, ws, static_cast<cudaStream_t>(stream)));
+}
+
 int moe_profile_events(void *const *events, int32_t n_events) {
   if (!events || n_events <= 0) {
     g_prof_on = false;

@@ -1,0 +1,183 @@
+// balance.cu -- sequence-wise balance loss and per-expert counts of packed
+// sequences (its gradient is part of the router's backward, router_bwd.cu).
+//
+// "DeepSeek-V3 Technischer Bericht" (xyznot.com/de), Methode section 2, in the
+// technical report's form.  For a sequence of L tokens:
+//   c_i = picks of expert i,  f_i = N_r / (K_r L) c_i,
+//   P_i = (1/L) sum_t s_{i,t} / sum_j s_{j,t},  loss = alpha sum_i f_i P_i.
+// Bound by reading the logit partials once.  A sequence may be as long as the
+// batch, so the tokens are cut into chunks that many CTAs take side by side; a
+// CTA sums the pieces of the sequences inside its chunk (piece c + s for chunk
+// c and sequence s: each chunk border and each sequence border starts a new
+// one), and one CTA per sequence adds its pieces in token order.  The result
+// does not depend on the schedule.
+#include "common.cuh"
+#include "kernels.h"
+#include "router_math.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int BAL_WARPS = 8;
+
+struct BalArgs {
+  const float *partial;
+  int n_ks;
+  int64_t T;
+  int Nr, Kr;
+  const int32_t *idx;
+  const int32_t *off;
+  int n_seq;
+  int chunk;      // tokens per chunk
+  int n_chunks;
+  float *p_part;  // [n_chunks + n_seq, Nr] sums of the normalised affinities
+  int32_t *c_part;  // [n_chunks + n_seq, Nr] picks
+  int32_t *err;
+};
+}  // namespace
+
+__global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const BalArgs a) {
+  __shared__ float p_sh[BAL_WARPS][EPL * 32];
+  __shared__ int c_sh[EPL * 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+  const int64_t c1 = c0 + a.chunk < a.T ? c0 + a.chunk : a.T;
+  bool bad = false;
+  int64_t t0 = c0;
+  while (t0 < c1) {  // every turn moves t0 forward, whatever the offsets hold
+    const int s = seq_of(a.off, a.n_seq, t0);
+    if (s >= a.n_seq) break;
+    if (a.off[s] > t0) {  // tokens before the first sequence belong to none
+      t0 = a.off[s];
+      continue;
+    }
+    const int64_t end = a.off[s + 1];
+    if (end <= t0) break;  // only with wrong offsets
+    const int64_t t1 = end < c1 ? end : c1;
+    float acc[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
+    for (int i = threadIdx.x; i < EPL * 32; i += blockDim.x) c_sh[i] = 0;
+    __syncthreads();
+    for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
+      float v[EPL];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 32 * i;
+        v[i] = e < a.Nr ? affinity(a.partial, a.n_ks, a.T, a.Nr, t, e) : 0.0f;
+        sum += v[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // all affinities 0 (every logit far below the exponential's range): no share
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      if (lane < a.Kr) {
+        const int e = a.idx[t * a.Kr + lane];
+        if (e >= 0 && e < a.Nr)
+          atomicAdd(&c_sh[e], 1);
+        else
+          bad = true;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) p_sh[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    const int64_t piece = static_cast<int64_t>(blockIdx.x) + s;
+    for (int e = threadIdx.x; e < a.Nr; e += blockDim.x) {
+      float p = 0.0f;
+#pragma unroll
+      for (int w = 0; w < BAL_WARPS; ++w) p += p_sh[w][e];
+      a.p_part[piece * a.Nr + e] = p;
+      a.c_part[piece * a.Nr + e] = c_sh[e];
+    }
+    __syncthreads();
+    t0 = t1;
+  }
+  if (bad) atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
+}
+
+// One CTA per sequence: four slices of 256 threads take every fourth piece.
+__global__ void __launch_bounds__(1024) balance_join_kernel(const BalArgs a, float alpha, float *__restrict__ loss,
+                                                             int32_t *__restrict__ counts) {
+  __shared__ float p_sh[4][256];
+  __shared__ int c_sh[4][256];
+  __shared__ float term[8];
+  const int s = blockIdx.x;
+  const int e = threadIdx.x & 255, sl = threadIdx.x >> 8;
+  int64_t b0 = a.off[s], b1 = a.off[s + 1];
+  if (b0 < 0 || b1 < b0 || b1 > a.T) {  // wrong offsets: reported, and read as an empty sequence
+    if (threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
+    b0 = b1 = 0;
+  }
+  float p = 0.0f;
+  int c = 0;
+  if (e < a.Nr && b1 > b0) {
+    const int64_t k0 = b0 / a.chunk, k1 = (b1 - 1) / a.chunk;
+    for (int64_t k = k0 + sl; k <= k1; k += 4) {
+      p += a.p_part[(k + s) * a.Nr + e];
+      c += a.c_part[(k + s) * a.Nr + e];
+    }
+  }
+  p_sh[sl][e] = p;
+  c_sh[sl][e] = c;
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    p = (p_sh[0][e] + p_sh[1][e]) + (p_sh[2][e] + p_sh[3][e]);
+    c = c_sh[0][e] + c_sh[1][e] + c_sh[2][e] + c_sh[3][e];
+    if (e < a.Nr) counts[static_cast<int64_t>(s) * a.Nr + e] = c;
+    float v = e < a.Nr ? static_cast<float>(c) * p : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) term[threadIdx.x >> 5] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float tot = 0.0f;
+    for (int i = 0; i < 8; ++i) tot += term[i];
+    const float L = static_cast<float>(b1 - b0);
+    loss[s] = b1 > b0 ? alpha * (static_cast<float>(a.Nr) / (static_cast<float>(a.Kr) * L)) * (tot / L) : 0.0f;
+  }
+}
+
+// Tokens per chunk: enough chunks to fill the SMs, at least BAL_WARPS tokens
+// each.
+int balance_chunk(int64_t T) {
+  const int64_t sms = moe_host::sm_count();
+  int64_t c = (T + 2 * sms - 1) / (2 * sms);
+  c = (c + BAL_WARPS - 1) / BAL_WARPS * BAL_WARPS;
+  return static_cast<int>(c < BAL_WARPS ? BAL_WARPS : c);
+}
+
+int64_t balance_pieces(int64_t T, int64_t n_seq) {
+  const int c = balance_chunk(T);
+  return (T + c - 1) / c + n_seq;
+}
+
+cudaError_t launch_balance_loss(const float *partial, int n_ks, int64_t T, int Nr, int Kr, const int32_t *idx,
+                                const int32_t *off, int n_seq, float alpha, float *p_part, int32_t *c_part,
+                                float *loss, int32_t *counts, int32_t *err, cudaStream_t st) {
+  if (n_seq == 0) return cudaSuccess;
+  BalArgs a{};
+  a.partial = partial;
+  a.n_ks = n_ks;
+  a.T = T;
+  a.Nr = Nr;
+  a.Kr = Kr;
+  a.idx = idx;
+  a.off = off;
+  a.n_seq = n_seq;
+  a.chunk = balance_chunk(T);
+  a.n_chunks = static_cast<int>((T + a.chunk - 1) / a.chunk);
+  a.p_part = p_part;
+  a.c_part = c_part;
+  a.err = err;
+  if (T > 0) balance_pieces_kernel<<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
+  if (const cudaError_t e = cudaGetLastError()) return e;
+  balance_join_kernel<<<n_seq, 1024, 0, st>>>(a, alpha, loss, counts);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

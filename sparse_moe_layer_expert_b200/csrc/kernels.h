@@ -193,6 +193,55 @@ cudaError_t launch_bias_update(float *bias, const int32_t *counts, int Nr, int64
                                cudaStream_t st);
 cudaError_t launch_wait_selftest(int32_t *err, uint64_t limit_ns, cudaStream_t st);
 
+// Residual addition + RMS norm + 1x128 quantization, and its backward
+// (norm.cu).  resid, h, w, y and rstd may be null; f32: the stream's type.
+cudaError_t launch_add_rmsnorm_quant(const void *x, int64_t ld_x, const void *resid, int64_t ld_r, bool f32,
+                                     const float *w, float eps, int64_t rows, int cols, void *h, void *y, uint8_t *q,
+                                     float *s, float *rstd, bool pow2, cudaStream_t st);
+// part: [norm_bwd_parts(rows, cols), cols] floats (when dw is given)
+int norm_bwd_parts(int64_t rows, int cols);
+cudaError_t launch_add_rmsnorm_bwd(const void *dy, bool dy_f32, const void *h, const void *dres, bool f32,
+                                   const float *w, const float *rstd, int64_t rows, int cols, void *dx, bool dx_f32,
+                                   float *dw, float *part, cudaStream_t st);
+
+// Balance loss and counts of packed sequences (balance.cu); p_part and c_part
+// hold balance_pieces(T, n_seq) x Nr values.
+int64_t balance_pieces(int64_t T, int64_t n_seq);
+cudaError_t launch_balance_loss(const float *partial, int n_ks, int64_t T, int Nr, int Kr, const int32_t *idx,
+                                const int32_t *off, int n_seq, float alpha, float *p_part, int32_t *c_part,
+                                float *loss, int32_t *counts, int32_t *err, cudaStream_t st);
+
+// Router backward (router_bwd.cu).
+struct RouterBwd {
+  const float *partial;  // logit partials [n_ks, T, Nr]
+  int n_ks;
+  int64_t T;
+  int Nr, Kr;
+  float route_scale;
+  const int32_t *idx;    // [T, Kr]
+  const float *dgate;    // [T, Kr] gradient of the gates, or null
+  const float *gdot;     // or gate * gradient: the sum of gdot[pos[t, k], 0 .. n_dot)
+  const int32_t *pos;
+  int n_dot;
+  const int32_t *off;    // [n_seq + 1], or null: no balance loss
+  int n_seq;
+  const int32_t *counts; // [n_seq, Nr]
+  const float *dloss;    // [n_seq] or null (ones)
+  float alpha;
+  float *dlogits;        // [T, Nr] or null
+  void *parts;           // bf16 [3, T, router_parts_pitch(Nr)] or null
+  int32_t *err;
+};
+int router_parts_pitch(int Nr);
+int router_dwr_split(int64_t T, int cols);
+int router_dwr_rows(int Nr);
+cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st);
+cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
+                             int32_t *err, uint64_t limit_ns, cudaStream_t st);
+// part: [router_dwr_split(T, H), router_dwr_rows(Nr), H] floats when the split is above 1
+cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
+                              int32_t *err, uint64_t limit_ns, cudaStream_t st);
+
 // weight-block pairs (tiles) per chunk of activations in each grouped GEMM
 __host__ __device__ inline int gemm1_blocks(int I) { return I / 128; }
 __host__ __device__ inline int gemm2_blocks(int H) { return (H / 128 + 1) / 2; }

@@ -17,6 +17,7 @@
 //     (a metric of the routing, outside the layer step).
 #include "common.cuh"
 #include "kernels.h"
+#include "router_math.cuh"
 
 namespace moe {
 
@@ -175,18 +176,6 @@ __global__ void __launch_bounds__(R_THREADS, 1)
 
 // ----------------------------------------------------------------- top-k
 namespace {
-constexpr int EPL = 8;  // experts per lane (N_r <= 256)
-
-// s_{e,t} from the router's logit partials: the K splits are added in split
-// order, then the sigmoid.  Every kernel that needs the affinities computes
-// them here, so they agree bit for bit.
-__device__ __forceinline__ float affinity(const float *__restrict__ partial, int n_ks, int64_t T, int Nr,
-                                          int64_t t, int e) {
-  float z = 0.0f;
-  for (int k = 0; k < n_ks; ++k) z += partial[(static_cast<int64_t>(k) * T + t) * Nr + e];
-  return 1.0f / (1.0f + expf(-z));
-}
-
 // Unsigned key with the order of the floats (-0 taken as +0), and back.
 __device__ __forceinline__ uint32_t ord_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
