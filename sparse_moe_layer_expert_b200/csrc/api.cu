@@ -30,18 +30,30 @@ int g_sms[kMaxDevices] = {0};
 int g_major[kMaxDevices] = {0};
 }  // namespace
 
+int encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int rank, const uint64_t *dims,
+                const uint64_t *strides, const uint32_t *box) {
+  std::call_once(g_encode_once, resolve_encode);
+  if (!g_encode || rank < 2 || rank > 5) return -1;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5];
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  const CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 int encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
-  std::call_once(g_encode_once, resolve_encode);
-  if (!g_encode) return -1;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r =
-      g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? 0 : -1;
+  const uint64_t dims[2] = {inner, outer};
+  const uint64_t strides[1] = {row_bytes};
+  const uint32_t box[2] = {box_inner, box_outer};
+  return encode_tmap(map, dtype, base, 2, dims, strides, box);
 }
 
 static int device_info(int *sms, int *major) {
@@ -1090,8 +1102,7 @@ struct RouterBwdLayout {
 void make_router_bwd_layout(const moe_config *c, int64_t T, RouterBwdLayout *L) {
   Carve cv;
   cv.take(L->parts, static_cast<size_t>(3) * T * moe::router_parts_pitch(c->n_routed) * 2);
-  const int64_t split = moe::router_dwr_split(T, c->hidden);
-  cv.take(L->dwr, split > 1 ? static_cast<size_t>(split) * moe::router_dwr_rows(c->n_routed) * c->hidden * 4 : 0);
+  cv.take(L->dwr, moe::router_dwr_scratch(T, c->hidden));
   L->total = (cv.off + 255) & ~size_t(255);
 }
 

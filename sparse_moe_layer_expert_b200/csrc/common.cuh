@@ -492,5 +492,9 @@ __device__ __forceinline__ uint8_t e4m3_rn_sat(float v) {
 namespace moe_host {
 int encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                    uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// Any rank up to 5: dims, strides (bytes, rank - 1 of them) and box innermost
+// first; 128-byte swizzle, zeros out of bounds.
+int encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int rank, const uint64_t *dims,
+                const uint64_t *strides, const uint32_t *box);
 int sm_count();
 }  // namespace moe_host

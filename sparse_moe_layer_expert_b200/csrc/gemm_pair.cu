@@ -360,34 +360,6 @@ std::atomic<int> *attr_done_clusters() {
   return n;
 }
 
-template <typename Fn>
-int64_t resident_pairs(Fn *fn, int smem, std::atomic<int> *cache) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) {
-    const int c = cache[dev].load(std::memory_order_acquire);
-    if (c > 0) return c;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(P_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
-    (void)cudaGetLastError();
-    n = moe_host::sm_count() / 2;
-  }
-  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_release);
-  return n;
-}
-
 template <int EPI>
 cudaError_t launch_pair_epi(const CUtensorMap &mw, const CUtensorMap &m0, const CUtensorMap &m1, const GemmArgs &a,
                             int64_t max_tiles, cudaStream_t st) {
@@ -395,7 +367,8 @@ cudaError_t launch_pair_epi(const CUtensorMap &mw, const CUtensorMap &m0, const 
   if (const cudaError_t e = smem_attr_once(gemm_pair_kernel<EPI>, P_SMEM, attr_done)) return e;
   // as many pairs as can be resident at once (persistent), fewer when there
   // are fewer tiles
-  const int64_t pairs = resident_pairs(gemm_pair_kernel<EPI>, P_SMEM, attr_done_clusters<EPI>());
+  const int64_t pairs = resident_pairs(gemm_pair_kernel<EPI>, P_THREADS, P_SMEM, moe_host::sm_count() / 2,
+                                       attr_done_clusters<EPI>());
   if (pairs <= 0) return cudaErrorLaunchOutOfResources;
   const int64_t ncl = max_tiles < pairs ? max_tiles : pairs;
   gemm_pair_kernel<EPI><<<static_cast<unsigned>(2 * ncl), P_THREADS, P_SMEM, st>>>(mw, m0, m1, a);

@@ -25,6 +25,37 @@ inline cudaError_t smem_attr_once(Fn *fn, int bytes, std::atomic<uint64_t> &done
   return e;
 }
 
+// Clusters of two CTAs of `threads` threads and `smem` bytes that fit on the
+// device at once, queried once per device (`cache`: 64 slots); `fallback` when
+// the query fails.
+template <typename Fn>
+inline int64_t resident_pairs(Fn *fn, int threads, int smem, int64_t fallback, std::atomic<int> *cache) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) {
+    const int c = cache[dev].load(std::memory_order_acquire);
+    if (c > 0) return c;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    n = static_cast<int>(fallback);
+  }
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_release);
+  return n;
+}
+
 // One unit of work of the grouped block-scaled GEMM, decoded on the device
 // from a chunk (<= 128 activation rows of one expert) and a weight-block pair.
 struct GemmTile {
@@ -233,12 +264,10 @@ struct RouterBwd {
   int32_t *err;
 };
 int router_parts_pitch(int Nr);
-int router_dwr_split(int64_t T, int cols);
-int router_dwr_rows(int Nr);
+size_t router_dwr_scratch(int64_t T, int cols);  // bytes of launch_router_dwr's part
 cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st);
 cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
                              int32_t *err, uint64_t limit_ns, cudaStream_t st);
-// part: [router_dwr_split(T, H), router_dwr_rows(Nr), H] floats when the split is above 1
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
                               int32_t *err, uint64_t limit_ns, cudaStream_t st);
 

@@ -48,13 +48,6 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
 constexpr uint32_t kIdescAMn = 1u << 15;
 constexpr uint32_t kIdescBMn = 1u << 16;
 
-__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
-               : "memory");
-}
-
 struct DzArgs {
   const float *partial;
   int n_ks;
@@ -182,28 +175,104 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
   }
 }
 
-// --------------------------------------------------------------- dx = dz W_r
+// ------------------------------------------------------ products, CTA pairs
+// Both products run on pairs of CTAs (two SMs, tcgen05 cta_group::2): M = 256
+// over the two CTAs, N = 256, each CTA holding half of A's rows and half of
+// B's, so an MMA reads 64 bytes of shared memory a cycle and SM (96 on a
+// single CTA's 128 x 256 tile) and the operands' arrival fits beside it.
 namespace {
 constexpr int kParts = 3;
-constexpr int RB_THREADS = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
-constexpr int RB_BOX = 128 * 128;  // one 32-column FP32 box of 128 rows
-constexpr int X_STAGES = 4;
-constexpr int X_A = 128 * 128;       // 128 tokens x 64 experts
-constexpr int X_BG = 64 * 128;       // 64 experts x 64 columns
-constexpr int X_B = 4 * 4 * X_BG;    // Np <= 256 experts x 256 columns
-constexpr int X_SMEM = 1024 + X_B + X_STAGES * X_A + 2 * RB_BOX + 256;
+constexpr int RP_THREADS = 384;  // warp 0 TMA, warp 1 MMA (even CTA), warps 4..11 epilogue
+
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// eight consecutive floats, one 32-byte sector
+__device__ __forceinline__ void st_f32x8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+// 3D and 4D tiled loads whose completion counts on an mbarrier of either CTA
+// of the pair (as tma_load_2d_pair).
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar_caddr, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_caddr), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar_caddr, int32_t x,
+                                                 int32_t y, int32_t z, int32_t w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_caddr), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+      : "memory");
+}
+
+struct PairUnits {  // this pair's units [u0, u1) of n * per, in order
+  int64_t u0, u1;
+};
+__host__ __device__ inline PairUnits pair_units(int pair, int pairs, int64_t units) {
+  return PairUnits{pair * units / pairs, (pair + 1) * units / pairs};
+}
+
+// --------------------------------------------------------------- dx = dz W_r
+// Units (256-column strip, 256-token tile), strip-major; a pair takes a run of
+// them.  The strip's W_r (Np experts x 256 columns, half in each CTA) stays in
+// shared memory for the run's tiles; the next strip's 64-expert blocks arrive
+// as the last tile's last pass over each of them ends.  The output goes out
+// through shared memory and TMA stores (or TMA adds, one per element): stores
+// of a TMEM row per thread, 32 bytes to each of 32 rows an instruction, kept
+// the L1 at 78% and took 12 us longer at T = 4096.
+constexpr int X_STAGES = 8;
+constexpr int X_A = 128 * 128;      // 128 tokens x 64 experts
+constexpr int X_BG = 64 * 128;      // 64 experts x 64 columns
+constexpr int X_KB = 4;             // 64-expert blocks at most
+constexpr int X_B = X_KB * 2 * X_BG;  // Np <= 256 experts x 128 columns
+constexpr int X_BOX = 128 * 128;    // 128 tokens x 32 FP32 columns
+constexpr int X_SMEM = 1024 + X_B + X_STAGES * X_A + 2 * X_BOX + 512;
 static_assert(X_SMEM <= 232448, "shared memory budget");
 
 struct DxArgs {
   int64_t T;
-  int n_tiles, m_tiles, cols;  // 256-column strips, 128-token tiles, H
-  int kb;                      // Np / 64
+  int n_strips, m_tiles, cols;  // H / 256 and T / 256, rounded up; H
+  int kb;                       // Np / 64
   int accumulate;
   int32_t *err;
   uint64_t limit_ns;
 };
 
-// 128 rows x 32 columns of FP32 per call: this thread's row `r` of the box.
+struct DxBars {
+  uint64_t full[X_STAGES];   // even CTA: the stage of both CTAs has landed
+  uint64_t empty[X_STAGES];  // each CTA: the MMAs have read the stage
+  uint64_t bfull[X_KB], bempty[X_KB];
+  uint64_t tfull[2], tempty[2];
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(DxBars) <= 512, "barrier block");
+
+// One 32-column box of 128 rows: this thread's row r, as the tensor map's
+// 128-byte swizzle expects it.
 __device__ __forceinline__ void put_box_row(uint8_t *box, int r, const uint32_t (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -212,299 +281,392 @@ __device__ __forceinline__ void put_box_row(uint8_t *box, int r, const uint32_t 
 }
 }  // namespace
 
-__global__ void __launch_bounds__(RB_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_o, const DxArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sb = smem, *sa = smem + X_B, *so = sa + X_STAGES * X_A;
-  uint64_t *full = reinterpret_cast<uint64_t *>(so + 2 * RB_BOX);
-  uint64_t *empty = full + X_STAGES;
-  uint64_t *bfull = empty + X_STAGES;
-  uint64_t *tfull = bfull + 1;
-  uint64_t *tempty = tfull + 2;
-  uint64_t *teardown = tempty + 2;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(teardown + 1);
-  int *abort_flag = reinterpret_cast<int *>(tmem_holder + 1);
+  uint8_t *sb = smem, *sa = sb + X_B, *so = sa + X_STAGES * X_A;
+  DxBars *bars = reinterpret_cast<DxBars *>(so + 2 * X_BOX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < X_STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&bars->full[i], 2);  // each CTA's producer announces its bytes
+      mbar_init(&bars->empty[i], 1);
     }
-    mbar_init(bfull, 1);
+    for (int i = 0; i < X_KB; ++i) {
+      mbar_init(&bars->bfull[i], 2);
+      mbar_init(&bars->bempty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 4);
+      mbar_init(&bars->tfull[i], 1);
+      mbar_init(&bars->tempty[i], 16);
     }
-    mbar_init(teardown, 1);
-    *abort_flag = 0;
+    mbar_init(&bars->teardown, 1);
+    bars->abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&map_o);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(&bars->tmem_base, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const WaitCtl ctl{abort_flag, args.err, args.limit_ns};
-  const int nt = blockIdx.x % args.n_tiles, j0 = blockIdx.x / args.n_tiles;
-  const int jn = gridDim.x / args.n_tiles;
+  const uint32_t tmem = bars->tmem_base;
+  volatile int *abortp = &bars->abort_flag;
+  const WaitCtl ctl{abortp, args.err, args.limit_ns};
+  const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, static_cast<int64_t>(args.n_strips) * args.m_tiles);
   const int kb = args.kb, nk = kParts * kb;
 
   if (warp == 0) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(bfull, kb * 4 * X_BG);
-      for (int b = 0; b < kb; ++b)
-        for (int g = 0; g < 4; ++g)
-          tma_load_2d(sb + (b * 4 + g) * X_BG, &map_w, bfull, nt * 256 + g * 64, b * 64);
-      uint32_t it = 0;
-      for (int m = j0; m < args.m_tiles && !*abort_flag; m += jn) {
+      const uint64_t pol = policy_evict_last();  // every strip reads the parts again
+      uint32_t it = 0, nb = 0;  // stages; strips
+      int64_t strip = -1;
+      bool stop = false;
+      for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u) {
+        if (*abortp) break;
+        const int m = static_cast<int>(u % args.m_tiles);
+        const bool fresh = u / args.m_tiles != strip;
+        strip = u / args.m_tiles;
+        for (int k = 0; k < nk && !stop; ++k, ++it) {
+          const int s = it % X_STAGES;
+          if (fresh && k < kb) {  // the strip's block of W_r that this step is the first to read
+            if (!mbar_wait(&bars->bempty[k], (nb & 1) ^ 1, ctl)) {
+              stop = true;
+              break;
+            }
+            const uint32_t bar = mapa_shared(smem_u32(&bars->bfull[k]), 0);
+            mbar_arrive_expect_tx_cluster(bar, 2 * X_BG);
+            for (int g = 0; g < 2; ++g)
+              tma_load_2d_pair(sb + (k * 2 + g) * X_BG, &map_w, bar,
+                               static_cast<int>(strip) * 256 + rank * 128 + g * 64, k * 64, pol);
+          }
+          if (!mbar_wait(&bars->empty[s], ((it / X_STAGES) & 1) ^ 1, ctl)) {
+            stop = true;
+            break;
+          }
+          const uint32_t bar = mapa_shared(smem_u32(&bars->full[s]), 0);
+          mbar_arrive_expect_tx_cluster(bar, X_A);
+          tma_load_2d_pair(sa + s * X_A, &map_a, bar, (k % kb) * 64,
+                           static_cast<int>((k / kb) * args.T + static_cast<int64_t>(m) * 256 + rank * 128), pol);
+        }
+        if (fresh) ++nb;
+      }
+      // the stages in flight are read before this CTA may exit
+      int quiet = 0;
+      const WaitCtl drain{&quiet, nullptr, 100000000ull};
+      const uint32_t n_inflight = it < X_STAGES ? it : X_STAGES;
+      for (uint32_t j = it - n_inflight; j < it; ++j) mbar_wait(&bars->empty[j % X_STAGES], (j / X_STAGES) & 1, drain);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, tc = 0, nb = 0;
+      int64_t strip = -1;
+      bool stop = false;
+      const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescBMn;
+      for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u, ++tc) {
+        if (*abortp) break;
+        const bool fresh = u / args.m_tiles != strip;
+        strip = u / args.m_tiles;
+        const bool last = u + 1 < pu.u1 && (u + 1) / args.m_tiles != strip;  // another strip follows
+        const uint32_t buf = tc & 1;
+        if (!mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) break;
+        const uint32_t d = tmem + buf * 256;
         for (int k = 0; k < nk; ++k, ++it) {
           const int s = it % X_STAGES;
-          if (!mbar_wait(&empty[s], ((it / X_STAGES) & 1) ^ 1, ctl)) break;
-          mbar_arrive_expect_tx(&full[s], X_A);
-          tma_load_2d(sa + s * X_A, &map_a, &full[s], (k % kb) * 64,
-                      static_cast<int>((k / kb) * args.T + static_cast<int64_t>(m) * 128));
-        }
-      }
-      // copies still in flight land before the CTA can exit
-      int quiet = 0;
-      const WaitCtl drain{&quiet, nullptr, 100000000ull};
-      mbar_wait(bfull, 0, drain);
-      const uint32_t n_inflight = it < X_STAGES ? it : X_STAGES;
-      for (uint32_t q = it - n_inflight; q < it; ++q) mbar_wait(&full[q % X_STAGES], (q / X_STAGES) & 1, drain);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, tc = 0;
-      const uint32_t idesc = idesc_bf16_f32(128, 256) | kIdescBMn;
-      if (mbar_wait(bfull, 0, ctl)) {
-        for (int m = j0; m < args.m_tiles && !*abort_flag; m += jn, ++tc) {
-          const uint32_t buf = tc & 1;
-          if (!mbar_wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) break;
-          tc_fence_after();
-          const uint32_t d = tmem + buf * 256;
-          for (int k = 0; k < nk; ++k, ++it) {
-            const int s = it % X_STAGES;
-            if (!mbar_wait(&full[s], (it / X_STAGES) & 1, ctl)) break;
-            tc_fence_after();
-            const uint64_t da = sw128_kmajor_desc(smem_u32(sa + s * X_A));
-            const uint64_t db = sw128_mnmajor_desc(smem_u32(sb + (k % kb) * 4 * X_BG), X_BG);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              umma_bf16(d, da + 2 * q, db + (2048 >> 4) * q, idesc, (k > 0 || q > 0) ? 1u : 0u);
-            umma_commit(&empty[s]);
+          if ((fresh && k < kb && !mbar_wait(&bars->bfull[k], nb & 1, ctl)) ||
+              !mbar_wait(&bars->full[s], (it / X_STAGES) & 1, ctl)) {
+            stop = true;
+            break;
           }
-          umma_commit(&tfull[buf]);
+          tc_fence_after();
+          const uint64_t da = sw128_kmajor_desc(smem_u32(sa + s * X_A));
+          const uint64_t db = sw128_mnmajor_desc(smem_u32(sb + (k % kb) * 2 * X_BG), X_BG);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            umma_bf16_pair(d, da + 2 * q, db + (2048 >> 4) * q, idesc, (k > 0 || q > 0) ? 1u : 0u);
+          umma_commit_pair(&bars->empty[s], 0x3);
+          if (last && k >= nk - kb) umma_commit_pair(&bars->bempty[k % kb], 0x3);
         }
+        umma_commit_pair(&bars->tfull[buf], 0x3);
+        if (fresh) ++nb;
       }
       int quiet = 0;
       const WaitCtl drain{&quiet, nullptr, 100000000ull};
-      umma_commit(teardown);
-      mbar_wait(teardown, 0, drain);
+      umma_commit_pair(&bars->teardown, 0x1);
+      mbar_wait(&bars->teardown, 0, drain);
     }
-  } else {
-    const int q = warp & 3;  // TMEM lane quarter
+  } else if (warp >= 4) {
+    const int q = warp & 3;          // TMEM lane quarter
+    const int wg = (warp - 4) >> 2;  // column half: its four warps share a box and named barrier 1 + wg
     const int r = q * 32 + lane;
-    const bool issuer = warp == 2 && lane == 0;
-    uint32_t tc = 0, nbox = 0;
-    for (int m = j0; m < args.m_tiles; m += jn, ++tc) {
+    const bool issuer = q == 0 && lane == 0;
+    uint8_t *box = so + wg * X_BOX;
+    uint32_t tc = 0;
+    for (int64_t u = pu.u0; u < pu.u1; ++u, ++tc) {
       const uint32_t buf = tc & 1;
-      const bool ok = mbar_wait(&tfull[buf], (tc >> 1) & 1, ctl);
-      // all four warps leave together (they meet at a barrier below)
-      if (named_bar_or(1, 128, !ok)) break;
+      const bool ok = mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl);
+      if (named_bar_or(1 + wg, 128, !ok)) break;  // the four warps leave together
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256;
+      const int y = static_cast<int>(u % args.m_tiles) * 256 + rank * 128;
+      const int x0 = static_cast<int>(u / args.m_tiles) * 256 + wg * 128;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
+      if (x0 < args.cols && y < args.T) {  // H is a multiple of 128: a column half is in or out
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        const int x = nt * 256 + c * 32;
-        if (x >= args.cols) break;
-        uint32_t v[32];
-        tmem_ld32(ta + c * 32, v);
-        tmem_ld_wait();
-        uint8_t *box = so + (nbox & 1) * RB_BOX;
-        if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        named_bar_sync(1, 128);
-        put_box_row(box, r, v);
-        fence_proxy_async_smem();
-        named_bar_sync(1, 128);
-        if (issuer) {
-          if (args.accumulate)
-            tma_reduce_add_2d(&map_o, box, x, m * 128);
-          else
-            tma_store_2d(&map_o, box, x, m * 128);
-          bulk_commit();
-        }
-        ++nbox;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
-    }
-    if (issuer) bulk_wait_all();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
-}
-
-// ------------------------------------------------------------ dW_r = dz^T x
-namespace {
-constexpr int WR_STAGES = 3;
-constexpr int WR_TOK = 32;                       // tokens (K) per stage
-constexpr int WR_G = WR_TOK * 128;               // 32 tokens x 64 experts (or columns)
-constexpr int WR_A = kParts * 4 * WR_G;
-constexpr int WR_B = 4 * WR_G;
-constexpr int WR_STAGE = WR_A + WR_B;
-constexpr int WR_SMEM = 1024 + WR_STAGES * WR_STAGE + 2 * RB_BOX + 256;
-static_assert(WR_SMEM <= 232448, "shared memory budget");
-
-struct DwrArgs {
-  int64_t T;
-  int n_tiles, n_split, cols;  // 256-column strips, token ranges, H
-  int ng;                      // Np / 64
-  int halves;                  // 128-expert halves
-  int out_rows;                // output rows per token range
-  int32_t *err;
-  uint64_t limit_ns;
-};
-}  // namespace
-
-__global__ void __launch_bounds__(RB_THREADS, 1)
-    router_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
-                      const __grid_constant__ CUtensorMap map_o, const DwrArgs args) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *so = smem + WR_STAGES * WR_STAGE;
-  uint64_t *full = reinterpret_cast<uint64_t *>(so + 2 * RB_BOX);
-  uint64_t *empty = full + WR_STAGES;
-  uint64_t *tfull = empty + WR_STAGES;
-  uint64_t *teardown = tfull + 1;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(teardown + 1);
-  int *abort_flag = reinterpret_cast<int *>(tmem_holder + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < WR_STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    mbar_init(tfull, 1);
-    mbar_init(teardown, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const WaitCtl ctl{abort_flag, args.err, args.limit_ns};
-  const int nt = blockIdx.x % args.n_tiles, js = blockIdx.x / args.n_tiles;
-  const int64_t nkb = (args.T + WR_TOK - 1) / WR_TOK;
-  const int kb0 = static_cast<int>(js * nkb / args.n_split), kb1 = static_cast<int>((js + 1) * nkb / args.n_split);
-
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % WR_STAGES;
-        if (!mbar_wait(&empty[s], ((it / WR_STAGES) & 1) ^ 1, ctl)) break;
-        uint8_t *st = smem + s * WR_STAGE;
-        mbar_arrive_expect_tx(&full[s], (kParts * args.ng + 4) * WR_G);
-        for (int g = 0; g < 4; ++g)
-          tma_load_2d(st + WR_A + g * WR_G, &map_x, &full[s], nt * 256 + g * 64, kb * WR_TOK);
-        for (int p = 0; p < kParts; ++p)
-          for (int g = 0; g < args.ng; ++g)
-            tma_load_2d(st + (p * 4 + g) * WR_G, &map_a, &full[s], g * 64,
-                        static_cast<int>(p * args.T + static_cast<int64_t>(kb) * WR_TOK));
-      }
-      int quiet = 0;
-      const WaitCtl drain{&quiet, nullptr, 100000000ull};
-      const uint32_t n_inflight = it < WR_STAGES ? it : WR_STAGES;
-      for (uint32_t q = it - n_inflight; q < it; ++q) mbar_wait(&full[q % WR_STAGES], (q / WR_STAGES) & 1, drain);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      const uint32_t idesc = idesc_bf16_f32(128, 256) | kIdescAMn | kIdescBMn;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % WR_STAGES;
-        if (!mbar_wait(&full[s], (it / WR_STAGES) & 1, ctl)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + s * WR_STAGE);
-#pragma unroll
-        for (int q = 0; q < WR_TOK / 16; ++q) {
-          const uint64_t db = sw128_mnmajor_desc(st + WR_A + q * 2048, WR_G);
-#pragma unroll
-          for (int p = 0; p < kParts; ++p)
-            for (int h = 0; h < args.halves; ++h)
-              umma_bf16(tmem + h * 256, sw128_mnmajor_desc(st + (p * 4 + h * 2) * WR_G + q * 2048, WR_G), db, idesc,
-                        (it > 0 || q > 0 || p > 0) ? 1u : 0u);
-        }
-        umma_commit(&empty[s]);
-      }
-      umma_commit(tfull);
-      int quiet = 0;
-      const WaitCtl drain{&quiet, nullptr, 100000000ull};
-      umma_commit(teardown);
-      mbar_wait(teardown, 0, drain);
-    }
-  } else {
-    const int q = warp & 3;
-    const int r = q * 32 + lane;
-    const bool issuer = warp == 2 && lane == 0;
-    const bool ok = mbar_wait(tfull, 0, ctl);
-    if (!named_bar_or(1, 128, !ok)) {
-      tc_fence_after();
-      uint32_t nbox = 0;
-      for (int h = 0; h < args.halves; ++h) {
-        const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const int x = nt * 256 + c * 32;
-          if (x >= args.cols) break;
+        for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(ta + c * 32, v);
           tmem_ld_wait();
-          uint8_t *box = so + (nbox & 1) * RB_BOX;
-          if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          named_bar_sync(1, 128);
+          if (issuer) bulk_wait_read();  // the box's last store has read it
+          named_bar_sync(1 + wg, 128);
           put_box_row(box, r, v);
           fence_proxy_async_smem();
-          named_bar_sync(1, 128);
+          named_bar_sync(1 + wg, 128);
           if (issuer) {
-            tma_store_2d(&map_o, box, x, js * args.out_rows + h * 128);
+            if (args.accumulate)
+              tma_reduce_add_2d(&map_o, box, x0 + c * 32, y);
+            else
+              tma_store_2d(&map_o, box, x0 + c * 32, y);
             bulk_commit();
           }
-          ++nbox;
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
     }
     if (issuer) bulk_wait_all();
   }
+  // neither CTA leaves (or frees TMEM) while the other still works with its
+  // shared memory, barriers or TMEM
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// part [n, rows, cols] -> out [Nr, cols], the ranges in order; 4 columns a thread
-__global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__ part, int n, int rows, int Nr,
-                                                        int cols, float *__restrict__ out) {
+// ------------------------------------------------------------ dW_r = dz^T x
+// Units (256-column strip of x, 64-token stage), strip-major; a pair takes a
+// run of them, so a strip's tokens are shared out over several pairs and every
+// SM has the same work.  The tensor core's FP32 accumulation drops the bits
+// below its 24 at every step (measured: the error grows with the number of
+// steps, to 6e-6 of the result over 3300 tokens), so one TMEM accumulator takes
+// WR_CHUNK stages (48 steps) at most: the epilogue warps add it into FP32
+// registers while the next chunk's MMAs fill the other buffer.  At the end of a
+// strip's run the registers go to the partial sums, piece (pair + strip).
+// A stage is two loads, one 4D box of the parts and one 3D box of x: as eight
+// 2D boxes of 32 tokens each load cost about 110 ns and set the pace.
+namespace {
+constexpr int WR_STAGES = 3;
+constexpr int WR_TOK = 64;                   // tokens (K) per stage
+constexpr int WR_CHUNK = 4;                  // stages per TMEM accumulation
+constexpr int WR_G = WR_TOK * 128;           // 64 tokens x 64 experts (or columns)
+constexpr int WR_A = kParts * 2 * WR_G;      // this CTA's 128 experts
+constexpr int WR_B = 2 * WR_G;               // this CTA's 128 columns
+constexpr int WR_STAGE = WR_A + WR_B;
+constexpr int WR_SMEM = 1024 + WR_STAGES * WR_STAGE + 256;
+static_assert(WR_SMEM <= 232448, "shared memory budget");
+
+// A pair's run [u, end) of one strip, and how its stages fall into chunks: the
+// MMA issuer and the epilogue walk it alike.
+__device__ __forceinline__ int64_t run_end(int64_t u, int64_t u1, int64_t per_strip) {
+  const int64_t e = (u / per_strip + 1) * per_strip;
+  return e < u1 ? e : u1;
+}
+
+struct DwrArgs {
+  int64_t T;
+  int n_strips, n_stages;  // H / 256 and T / 64, rounded up
+  int Nr;
+  float *part;             // [pairs + n_strips, 256, 256]
+  int32_t *err;
+  uint64_t limit_ns;
+};
+
+struct DwrBars {
+  uint64_t full[WR_STAGES];
+  uint64_t empty[WR_STAGES];
+  uint64_t tfull[2], tempty[2];
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(DwrBars) <= 256, "barrier block");
+}  // namespace
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
+    router_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                      const DwrArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DwrBars *bars = reinterpret_cast<DwrBars *>(smem + WR_STAGES * WR_STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WR_STAGES; ++i) {
+      mbar_init(&bars->full[i], 2);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->tfull[i], 1);
+      mbar_init(&bars->tempty[i], 16);
+    }
+    mbar_init(&bars->teardown, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_x);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&bars->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int *abortp = &bars->abort_flag;
+  const WaitCtl ctl{abortp, args.err, args.limit_ns};
+  const int pair = blockIdx.x >> 1;
+  const PairUnits pu = pair_units(pair, gridDim.x >> 1, static_cast<int64_t>(args.n_strips) * args.n_stages);
+
+  // Register split as in gemm_pair.cu: 128 * 72 + 256 * 216 = 384 * 168
+  if (warp < 4) {
+    setmaxnreg_dec<72>();
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint64_t pol_a = policy_evict_last();   // every strip reads the parts again
+        const uint64_t pol_x = policy_evict_first();  // x is read once
+        uint32_t it = 0;
+        for (int64_t u = pu.u0; u < pu.u1; ++u, ++it) {
+          const int s = it % WR_STAGES;
+          if (*abortp || !mbar_wait(&bars->empty[s], ((it / WR_STAGES) & 1) ^ 1, ctl)) break;
+          uint8_t *st = smem + s * WR_STAGE;
+          const uint32_t bar = mapa_shared(smem_u32(&bars->full[s]), 0);
+          const int t0 = static_cast<int>(u % args.n_stages) * WR_TOK;
+          mbar_arrive_expect_tx_cluster(bar, WR_STAGE);
+          tma_load_3d_pair(st + WR_A, &map_x, bar, 0, t0, static_cast<int>(u / args.n_stages) * 4 + rank * 2, pol_x);
+          tma_load_4d_pair(st, &map_a, bar, 0, t0, rank * 2, 0, pol_a);
+        }
+        int quiet = 0;
+        const WaitCtl drain{&quiet, nullptr, 100000000ull};
+        const uint32_t n_inflight = it < WR_STAGES ? it : WR_STAGES;
+        for (uint32_t j = it - n_inflight; j < it; ++j)
+          mbar_wait(&bars->empty[j % WR_STAGES], (j / WR_STAGES) & 1, drain);
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        uint32_t it = 0, tc = 0;
+        bool stop = false;
+        const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescAMn | kIdescBMn;
+        for (int64_t u = pu.u0; u < pu.u1 && !stop;) {
+          const int64_t end = run_end(u, pu.u1, args.n_stages);
+          for (; u < end && !stop; ++tc) {
+            const uint32_t buf = tc & 1;
+            if (*abortp || !mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) {
+              stop = true;
+              break;
+            }
+            const uint32_t d = tmem + buf * 256;
+            for (int k = 0; k < WR_CHUNK && u < end; ++k, ++u, ++it) {
+              const int s = it % WR_STAGES;
+              if (!mbar_wait(&bars->full[s], (it / WR_STAGES) & 1, ctl)) {
+                stop = true;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t st = smem_u32(smem + s * WR_STAGE);
+#pragma unroll
+              for (int q = 0; q < WR_TOK / 16; ++q) {
+                const uint64_t db = sw128_mnmajor_desc(st + WR_A + q * 2048, WR_G);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                  umma_bf16_pair(d, sw128_mnmajor_desc(st + p * 2 * WR_G + q * 2048, WR_G), db, idesc,
+                                 (k > 0 || q > 0 || p > 0) ? 1u : 0u);
+              }
+              umma_commit_pair(&bars->empty[s], 0x3);
+            }
+            umma_commit_pair(&bars->tfull[buf], 0x3);
+          }
+        }
+        int quiet = 0;
+        const WaitCtl drain{&quiet, nullptr, 100000000ull};
+        umma_commit_pair(&bars->teardown, 0x1);
+        mbar_wait(&bars->teardown, 0, drain);
+      }
+    }
+  } else {
+    setmaxnreg_inc<216>();
+    const int q = warp & 3;
+    const int wg = (warp - 4) >> 2;
+    const int row = rank * 128 + q * 32 + lane;          // expert
+    const bool live = rank * 128 + q * 32 < args.Nr;     // any expert in this warp
+    uint32_t tc = 0;
+    bool stop = false;
+    for (int64_t u = pu.u0; u < pu.u1 && !stop;) {
+      const int64_t strip = u / args.n_stages;
+      const int64_t end = run_end(u, pu.u1, args.n_stages);
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (; u < end; u += WR_CHUNK, ++tc) {
+        const uint32_t buf = tc & 1;
+        if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) {
+          stop = true;
+          break;
+        }
+        if (live) {
+          tc_fence_after();
+          const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[64];
+            tmem_ld64(ta + c * 64, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[c * 64 + j] += __uint_as_float(v[j]);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
+      }
+      if (row < args.Nr) {
+        float *o = args.part + ((pair + strip) * 256 + row) * 256 + wg * 128;
+#pragma unroll
+        for (int j = 0; j < 128; j += 8) st_f32x8(o + j, acc + j);
+      }
+      u = end;
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// dW_r [Nr, cols] from the pieces of each strip, in token order; 4 columns a
+// thread.
+__global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__ part, int pairs, int n_strips,
+                                                        int n_stages, int Nr, int cols, float *__restrict__ out) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4;
   if (i >= static_cast<int64_t>(Nr) * cols) return;
-  const int64_t stride = static_cast<int64_t>(rows) * cols;
-  float4 s = *reinterpret_cast<const float4 *>(part + i);
-  for (int k = 1; k < n; ++k) {
-    const float4 v = *reinterpret_cast<const float4 *>(part + k * stride + i);
+  const int e = static_cast<int>(i / cols), c = static_cast<int>(i % cols);
+  const int strip = c >> 8;
+  const int64_t units = static_cast<int64_t>(n_strips) * n_stages;
+  const int64_t a = static_cast<int64_t>(strip) * n_stages, b = a + n_stages;  // the strip's units
+  int p = static_cast<int>(a * pairs / units);  // a pair at or before the first one with a share
+  while (pair_units(p, pairs, units).u1 <= a) ++p;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (; p < pairs && pair_units(p, pairs, units).u0 < b; ++p) {
+    const float4 v = *reinterpret_cast<const float4 *>(part + ((static_cast<int64_t>(p) + strip) * 256 + e) * 256 +
+                                                       (c & 255));
     s.x += v.x;
     s.y += v.y;
     s.z += v.z;
@@ -516,15 +678,24 @@ __global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__
 // -------------------------------------------------------------------- host
 int router_parts_pitch(int Nr) { return (Nr + 63) / 64 * 64; }
 
-// Token ranges of the dW_r product: as many as fill the SMs in one wave.
-int router_dwr_split(int64_t T, int cols) {
-  const int n_tiles = (cols + 255) / 256;
-  const int64_t nkb = (T + WR_TOK - 1) / WR_TOK;
-  int64_t j = moe_host::sm_count() / n_tiles;
-  if (j > nkb) j = nkb;
-  return static_cast<int>(j < 1 ? 1 : j);
+
+namespace {
+// Pairs of CTAs at most (one CTA per SM); a launch takes as many as are
+// resident at once.
+int64_t most_pairs() { return moe_host::sm_count() / 2; }
+
+int dwr_stages(int64_t T) { return static_cast<int>((T + WR_TOK - 1) / WR_TOK); }
+int strips_of(int cols) { return (cols + 255) / 256; }
+
+int dwr_pairs(int64_t T, int cols) {
+  const int64_t units = static_cast<int64_t>(strips_of(cols)) * dwr_stages(T);
+  return static_cast<int>(units < most_pairs() ? units : most_pairs());
 }
-int router_dwr_rows(int Nr) { return (Nr + 127) / 128 * 128; }
+}  // namespace
+
+size_t router_dwr_scratch(int64_t T, int cols) {
+  return T == 0 ? 0 : static_cast<size_t>(dwr_pairs(T, cols) + strips_of(cols)) * 256 * 256 * sizeof(float);
+}
 
 cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
   if (g.T == 0) return cudaSuccess;
@@ -568,53 +739,54 @@ cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int N
   DxArgs a{};
   a.T = T;
   a.cols = H;
-  a.n_tiles = (H + 255) / 256;
-  a.m_tiles = static_cast<int>((T + 127) / 128);
+  a.n_strips = strips_of(H);
+  a.m_tiles = static_cast<int>((T + 255) / 256);
   a.kb = Np / 64;
   a.accumulate = accumulate;
   a.err = err;
   a.limit_ns = limit_ns;
   static std::atomic<uint64_t> attr_done{0};
   if (const cudaError_t e = smem_attr_once(router_dx_kernel, X_SMEM, attr_done)) return e;
-  int j = moe_host::sm_count() / a.n_tiles;
-  if (j > a.m_tiles) j = a.m_tiles;
-  if (j < 1) j = 1;
-  router_dx_kernel<<<a.n_tiles * j, RB_THREADS, X_SMEM, st>>>(ma, mw, mo, a);
+  const int64_t units = static_cast<int64_t>(a.n_strips) * a.m_tiles;
+  static std::atomic<int> resident[64];
+  int64_t pairs = resident_pairs(router_dx_kernel, RP_THREADS, X_SMEM, most_pairs(), resident);
+  if (pairs > units) pairs = units;
+  if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  router_dx_kernel<<<static_cast<unsigned>(2 * pairs), RP_THREADS, X_SMEM, st>>>(ma, mw, mo, a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
                               int32_t *err, uint64_t limit_ns, cudaStream_t st) {
   if (T == 0) return cudaMemsetAsync(dwr, 0, sizeof(float) * Nr * static_cast<size_t>(H), st);
-  const int Np = router_parts_pitch(Nr);
+  const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
   DwrArgs a{};
   a.T = T;
-  a.cols = H;
-  a.n_tiles = (H + 255) / 256;
-  a.n_split = router_dwr_split(T, H);
-  a.ng = Np / 64;
-  a.halves = (Nr + 127) / 128;
-  a.out_rows = router_dwr_rows(Nr);
+  a.n_strips = strips_of(H);
+  a.n_stages = dwr_stages(T);
+  a.Nr = Nr;
+  a.part = part;
   a.err = err;
   a.limit_ns = limit_ns;
-  const bool join = a.n_split > 1;
-  CUtensorMap ma, mx, mo;
-  if (moe_host::encode_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, Np, kParts * T,
-                               static_cast<uint64_t>(Np) * 2, 64, WR_TOK) != 0 ||
-      moe_host::encode_tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, H, T, static_cast<uint64_t>(H) * 2, 64,
-                               WR_TOK) != 0 ||
-      moe_host::encode_tmap_2d(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, join ? part : dwr, H,
-                               join ? static_cast<uint64_t>(a.n_split) * a.out_rows : Nr,
-                               static_cast<uint64_t>(H) * 4, 32, 128) != 0)
+  // both operands in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], x [H / 64][T][64]
+  const uint64_t da[4] = {64, t, Np / 64, kParts}, sa[3] = {Np * 2, 128, t * Np * 2};
+  const uint64_t dx[3] = {64, t, h / 64}, sx[2] = {h * 2, 128};
+  const uint32_t ba[4] = {64, WR_TOK, 2, kParts}, bx[3] = {64, WR_TOK, 2};
+  CUtensorMap ma, mx;
+  if (moe_host::encode_tmap(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, 4, da, sa, ba) != 0 ||
+      moe_host::encode_tmap(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dx, sx, bx) != 0)
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr_done{0};
   if (const cudaError_t e = smem_attr_once(router_dwr_kernel, WR_SMEM, attr_done)) return e;
-  router_dwr_kernel<<<a.n_tiles * a.n_split, RB_THREADS, WR_SMEM, st>>>(ma, mx, mo, a);
+  static std::atomic<int> resident[64];
+  int64_t pairs = resident_pairs(router_dwr_kernel, RP_THREADS, WR_SMEM, most_pairs(), resident);
+  if (pairs > dwr_pairs(T, H)) pairs = dwr_pairs(T, H);
+  if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  router_dwr_kernel<<<static_cast<unsigned>(2 * pairs), RP_THREADS, WR_SMEM, st>>>(ma, mx, a);
   if (const cudaError_t e = cudaGetLastError()) return e;
-  if (join) {
-    const int64_t n4 = static_cast<int64_t>(Nr) * H / 4;
-    dwr_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, st>>>(part, a.n_split, a.out_rows, Nr, H, dwr);
-  }
+  const int64_t n4 = static_cast<int64_t>(Nr) * H / 4;
+  dwr_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, st>>>(part, static_cast<int>(pairs), a.n_strips,
+                                                                         a.n_stages, Nr, H, dwr);
   return cudaGetLastError();
 }
 
