@@ -36,8 +36,9 @@ struct BalArgs {
 };
 }  // namespace
 
+template <bool VEC>
 __global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const BalArgs a) {
-  __shared__ float p_sh[BAL_WARPS][EPL * 32];
+  __shared__ __align__(16) float p_sh[BAL_WARPS][EPL * 32];
   __shared__ int c_sh[EPL * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
@@ -60,22 +61,24 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const Ba
     for (int i = threadIdx.x; i < EPL * 32; i += blockDim.x) c_sh[i] = 0;
     __syncthreads();
     for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
+      int e = 0;
+      if (lane < a.Kr) e = a.idx[t * a.Kr + lane];
       float v[EPL];
+      load_logits<VEC>(a.partial, a.n_ks, a.T, a.Nr, t, lane, v);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < a.Nr ? affinity(a.partial, a.n_ks, a.T, a.Nr, t, e) : 0.0f;
+        float om;
+        sigmoid_pair(v[i], v[i], om);
+        if (lane_expert(lane, i) >= a.Nr) v[i] = 0.0f;
         sum += v[i];
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = warp_sum(sum);
       // all affinities 0 (every logit far below the exponential's range): no share
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
       if (lane < a.Kr) {
-        const int e = a.idx[t * a.Kr + lane];
         if (e >= 0 && e < a.Nr)
           atomicAdd(&c_sh[e], 1);
         else
@@ -83,7 +86,9 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const Ba
       }
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) p_sh[warp][lane + 32 * i] = acc[i];
+    for (int g = 0; g < 2; ++g)
+      *reinterpret_cast<float4 *>(&p_sh[warp][g * 128 + lane * 4]) =
+          make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
     __syncthreads();
     const int64_t piece = static_cast<int64_t>(blockIdx.x) + s;
     for (int e = threadIdx.x; e < a.Nr; e += blockDim.x) {
@@ -142,11 +147,11 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const BalArgs a, flo
   }
 }
 
-// Tokens per chunk: enough chunks to fill the SMs, at least BAL_WARPS tokens
-// each.
+// Tokens per chunk: enough chunks for four CTAs on every SM, at least BAL_WARPS
+// tokens each.
 int balance_chunk(int64_t T) {
   const int64_t sms = moe_host::sm_count();
-  int64_t c = (T + 2 * sms - 1) / (2 * sms);
+  int64_t c = (T + 4 * sms - 1) / (4 * sms);
   c = (c + BAL_WARPS - 1) / BAL_WARPS * BAL_WARPS;
   return static_cast<int>(c < BAL_WARPS ? BAL_WARPS : c);
 }
@@ -174,7 +179,12 @@ cudaError_t launch_balance_loss(const float *partial, int n_ks, int64_t T, int N
   a.p_part = p_part;
   a.c_part = c_part;
   a.err = err;
-  if (T > 0) balance_pieces_kernel<<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
+  if (T > 0) {
+    if (Nr % 4 == 0)
+      balance_pieces_kernel<true><<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
+    else
+      balance_pieces_kernel<false><<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
+  }
   if (const cudaError_t e = cudaGetLastError()) return e;
   balance_join_kernel<<<n_seq, 1024, 0, st>>>(a, alpha, loss, counts);
   return cudaGetLastError();

@@ -17,7 +17,7 @@
 // parts would leave an error of 2^-17 of each term.
 //
 // Kernels:
-//   router_dz_kernel   one warp per token: dz, written in FP32 (when asked
+//   router_dz_kernel   a warp per run of tokens: dz, written in FP32 (when asked
 //                      for) and as parts [3][T][Np] bf16, Np = N_r rounded up
 //                      to 64 (zeros behind N_r)
 //   router_dx_kernel   persistent over 128-token tiles of one 256-column strip
@@ -67,110 +67,153 @@ struct DzArgs {
   float *dlogits;                // or null
   __nv_bfloat16 *parts;          // or null
   int Np;
+  int run;  // tokens per warp
   int32_t *err;
 };
 
-// v = hi + mid + lo, each the leading 8 significand bits of what is left
-__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
+// v = hi + mid + lo, each the leading 8 significand bits of what is left, as
+// bf16 in the upper half of o[k]
+__device__ __forceinline__ void split3(float v, uint32_t (&o)[3]) {
   const bool inf = (__float_as_uint(v) & 0x7FFFFFFFu) == 0x7F800000u;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const uint32_t u = __float_as_uint(v) & 0xFFFF0000u;
-    o[k] = __ushort_as_bfloat16(static_cast<unsigned short>(u >> 16));
-    v = inf ? 0.0f : v - __uint_as_float(u);
+    o[k] = __float_as_uint(v) & 0xFFFF0000u;
+    v = inf ? 0.0f : v - __uint_as_float(o[k]);
   }
 }
 
 }  // namespace
 
+// A warp takes `run` consecutive tokens; the load factors f of the sequence it
+// is in stay in registers from token to token.
+template <bool VEC>
 __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (t >= a.T) return;
-  float dz[EPL];
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t t0 = w * a.run, t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
+  int seq = -1;           // sequence whose f is held
+  int64_t seq_end = t0;   // look for a sequence at the first token
+  float f[EPL], kk = 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) dz[i] = 0.0f;
-  if (a.off) {
-    const int s = seq_of(a.off, a.n_seq, t);
-    if (s < a.n_seq && a.off[s] <= t) {
-      const float L = static_cast<float>(static_cast<int64_t>(a.off[s + 1]) - a.off[s]);
-      const float fl = static_cast<float>(a.Nr) / (static_cast<float>(a.Kr) * L);
-      const float kk = (a.dloss ? a.dloss[s] : 1.0f) * (a.alpha / L);
-      float v[EPL], f[EPL], om[EPL];
-      float sum = 0.0f;
+  for (int i = 0; i < EPL; ++i) f[i] = 0.0f;
+  for (int64_t t = t0; t < t1; ++t) {
+    float dz[EPL];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = f[i] = om[i] = 0.0f;
-        if (e < a.Nr) {
-          affinity_pair(a.partial, a.n_ks, a.T, a.Nr, t, e, v[i], om[i]);
-          f[i] = fl * static_cast<float>(a.counts[static_cast<int64_t>(s) * a.Nr + e]);
-        }
-        sum += v[i];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      float fp = 0.0f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        v[i] *= inv;
-        fp = fmaf(f[i], v[i], fp);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) fp += __shfl_xor_sync(0xffffffffu, fp, o);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) dz[i] = kk * (v[i] * om[i]) * (f[i] - fp);
-    }
-  }
-  if (a.dgate || a.gdot) {
-    // lane r holds slot r
+    for (int i = 0; i < EPL; ++i) dz[i] = 0.0f;
+    // the slots' indices and gradients, asked for before they are needed (lane r: slot r)
     int e = -1;
-    float s = 0.0f, om = 0.0f;
-    if (lane < a.Kr) {
+    float w_k = 0.0f;
+    if ((a.dgate || a.gdot) && lane < a.Kr) {
       e = a.idx[t * a.Kr + lane];
-      if (e < 0 || e >= a.Nr) {
-        atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
-        e = -1;
+      if (a.dgate) w_k = a.dgate[t * a.Kr + lane];
+    }
+    if (a.off) {
+      float z[EPL];
+      load_logits<VEC>(a.partial, a.n_ks, a.T, a.Nr, t, lane, z);
+      if (t >= seq_end) {
+        const int s = seq_of(a.off, a.n_seq, t);
+        seq = -1;
+        seq_end = a.T;
+        if (s < a.n_seq) {
+          const int64_t b0 = a.off[s], b1 = a.off[s + 1];
+          if (b0 <= t) {
+            seq = s;
+            seq_end = b1;
+            const float L = static_cast<float>(b1 - b0);
+            const float fl = static_cast<float>(a.Nr) / (static_cast<float>(a.Kr) * L);
+            kk = (a.dloss ? a.dloss[s] : 1.0f) * (a.alpha / L);
+            const int32_t *cnt = a.counts + static_cast<int64_t>(s) * a.Nr;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              f[i] = lane_expert(lane, i) < a.Nr ? fl * static_cast<float>(cnt[lane_expert(lane, i)]) : 0.0f;
+          } else {
+            seq_end = b0;  // before the first sequence
+          }
+        }
+      }
+      if (seq >= 0) {
+        float sum = 0.0f, fp = 0.0f, po[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          float s, om;
+          sigmoid_pair(z[i], s, om);
+          if (lane_expert(lane, i) >= a.Nr) s = 0.0f;
+          sum += s;
+          fp = fmaf(f[i], s, fp);
+          po[i] = s * om;
+        }
+        sum = warp_sum(sum);
+        fp = warp_sum(fp);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        fp *= inv;
+        const float c = kk * inv;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) dz[i] = c * po[i] * (f[i] - fp);
       }
     }
-    if (e >= 0) affinity_pair(a.partial, a.n_ks, a.T, a.Nr, t, e, s, om);
-    float sum = s;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float gh = sum > 0.0f ? s / sum : 0.0f;
-    float w = 0.0f;  // a_k
-    if (e >= 0) {
+    if (a.dgate || a.gdot) {
+      float s = 0.0f, om = 0.0f;
+      if (lane < a.Kr) {
+        if (e < 0 || e >= a.Nr) {
+          atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
+          e = -1;
+        } else {
+          float z = 0.0f;
+          for (int k = 0; k < a.n_ks; ++k) z += __ldg(a.partial + (static_cast<int64_t>(k) * a.T + t) * a.Nr + e);
+          sigmoid_pair(z, s, om);
+        }
+      }
+      const float sum = warp_sum(s);
+      const float gh = sum > 0.0f ? s / sum : 0.0f;
       if (a.gdot) {
-        const float *d = a.gdot + static_cast<int64_t>(a.pos[t * a.Kr + lane]) * a.n_dot;
-        for (int j = 0; j < a.n_dot; ++j) w += d[j];
+        w_k = 0.0f;
+        if (e >= 0) {
+          const float *d = a.gdot + static_cast<int64_t>(a.pos[t * a.Kr + lane]) * a.n_dot;
+          for (int j = 0; j < a.n_dot; ++j) w_k += d[j];
+        }
       } else {
-        w = a.route_scale * a.dgate[t * a.Kr + lane] * gh;
+        w_k = e >= 0 ? a.route_scale * w_k * gh : 0.0f;  // a_k
+      }
+      const float tot = warp_sum(w_k);
+      const float d = om * (w_k - gh * tot);
+      for (int r = 0; r < a.Kr; ++r) {
+        const int er = __shfl_sync(0xffffffffu, e, r);
+        const float dr = __shfl_sync(0xffffffffu, d, r);
+        if (er >= 0 && ((er & 127) >> 2) == lane) {
+          const int at = (er >> 7) * 4 + (er & 3);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (i == at) dz[i] += dr;
+        }
       }
     }
-    float tot = w;
+    if (a.dlogits) {
+      float *row = a.dlogits + t * a.Nr;
+      if (VEC && (reinterpret_cast<uintptr_t>(a.dlogits) & 15) == 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    const float d = om * (w - gh * tot);
-    for (int r = 0; r < a.Kr; ++r) {
-      const int er = __shfl_sync(0xffffffffu, e, r);
-      const float dr = __shfl_sync(0xffffffffu, d, r);
-      if (er >= 0 && (er & 31) == lane) {
+        for (int g = 0; g < 2; ++g)
+          if (g * 128 + lane * 4 < a.Nr)
+            *reinterpret_cast<float4 *>(row + g * 128 + lane * 4) =
+                make_float4(dz[4 * g], dz[4 * g + 1], dz[4 * g + 2], dz[4 * g + 3]);
+      } else {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (i == (er >> 5)) dz[i] += dr;
+          if (lane_expert(lane, i) < a.Nr) row[lane_expert(lane, i)] = dz[i];
       }
     }
-  }
+    if (a.parts) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    if (a.dlogits && e < a.Nr) a.dlogits[t * a.Nr + e] = dz[i];
-    if (a.parts && e < a.Np) {
-      __nv_bfloat16 o[3];
-      split3(e < a.Nr ? dz[i] : 0.0f, o);
+      for (int g = 0; g < 2; ++g) {
+        if (g * 128 + lane * 4 < a.Np) {  // Np is a multiple of 64; dz is 0 behind N_r
+          uint32_t p[4][3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) a.parts[(static_cast<int64_t>(k) * a.T + t) * a.Np + e] = o[k];
+          for (int j = 0; j < 4; ++j) split3(dz[4 * g + j], p[j]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint2 *>(a.parts + (static_cast<int64_t>(k) * a.T + t) * a.Np + g * 128 + lane * 4) =
+                make_uint2(__byte_perm(p[0][k], p[1][k], 0x7632), __byte_perm(p[2][k], p[3][k], 0x7632));
+        }
+      }
     }
   }
 }
@@ -720,7 +763,15 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
   a.parts = static_cast<__nv_bfloat16 *>(g.parts);
   a.Np = router_parts_pitch(g.Nr);
   a.err = g.err;
-  router_dz_kernel<<<static_cast<unsigned>((g.T + 7) / 8), 256, 0, st>>>(a);
+  // four warps per scheduler at once, and no more tokens per warp than that takes
+  const int64_t warps = static_cast<int64_t>(moe_host::sm_count()) * 32;
+  const int64_t run = (g.T + warps - 1) / warps;
+  a.run = static_cast<int>(run < 8 ? run : 8);
+  const unsigned grid = static_cast<unsigned>(((g.T + a.run - 1) / a.run + 7) / 8);
+  if (g.Nr % 4 == 0)
+    router_dz_kernel<true><<<grid, 256, 0, st>>>(a);
+  else
+    router_dz_kernel<false><<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

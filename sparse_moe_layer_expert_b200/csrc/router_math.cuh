@@ -19,15 +19,54 @@ __device__ __forceinline__ float affinity(const float *__restrict__ partial, int
   return 1.0f / (1.0f + expf(-z));
 }
 
+// A warp's view of one token's N_r <= 256 experts: lane l holds the experts
+// 128 g + 4 l + j as element 4 g + j (g = 0, 1; j = 0..3), so a row is read
+// and written 16 bytes a lane.
+__device__ __forceinline__ int lane_expert(int lane, int i) { return (i >> 2) * 128 + lane * 4 + (i & 3); }
+
+// The token's logits: the K splits are added in split order (as affinity()),
+// every split's loads issued together.  VEC: N_r % 4 == 0 (16-byte loads).
+// Experts behind N_r give 0.
+template <bool VEC>
+__device__ __forceinline__ void load_logits(const float *__restrict__ partial, int n_ks, int64_t T, int Nr, int64_t t,
+                                            int lane, float (&z)[EPL]) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) z[i] = 0.0f;
+#pragma unroll 2
+  for (int k = 0; k < n_ks; ++k) {
+    const float *row = partial + (static_cast<int64_t>(k) * T + t) * Nr;
+    if (VEC) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g * 128 + lane * 4 < Nr) {
+          const float4 v = __ldg(reinterpret_cast<const float4 *>(row + g * 128 + lane * 4));
+          z[4 * g] += v.x;
+          z[4 * g + 1] += v.y;
+          z[4 * g + 2] += v.z;
+          z[4 * g + 3] += v.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane_expert(lane, i) < Nr) z[i] += __ldg(row + lane_expert(lane, i));
+    }
+  }
+}
+
 // s and 1 - s.  For z >= 0, 1 - s = e^-z s (1 - s itself would cancel); below,
-// s < 1/2 and the difference keeps its digits.
-__device__ __forceinline__ void affinity_pair(const float *__restrict__ partial, int n_ks, int64_t T, int Nr,
-                                              int64_t t, int e, float &s, float &om) {
-  float z = 0.0f;
-  for (int k = 0; k < n_ks; ++k) z += partial[(static_cast<int64_t>(k) * T + t) * Nr + e];
+// s < 1/2 and the difference keeps its digits.  The reciprocal is the
+// hardware's (1 ulp), as these feed gradients and sums, not the selection.
+__device__ __forceinline__ void sigmoid_pair(float z, float &s, float &om) {
   const float q = expf(-z);
-  s = 1.0f / (1.0f + q);
+  s = __fdividef(1.0f, 1.0f + q);  // q = inf gives 0
   om = z >= 0.0f ? q * s : 1.0f - s;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // The first sequence that ends behind token t (n_seq if none does): sequence
