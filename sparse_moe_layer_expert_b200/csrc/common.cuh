@@ -418,6 +418,13 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Eight consecutive floats, one 32-byte sector (p 32-byte aligned).
+__device__ __forceinline__ void st_f32x8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // a / b rounded to nearest from y = RN(1/b): q0 = RN(a*y), the exact residual
 // r = a - b*q0 (one FMA), then RN(q0 + r*y).  One residual correction of the
 // quotient (Markstein's division by reciprocal, as presented in Muller et al.,

@@ -50,8 +50,21 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
   *reinterpret_cast<uint4 *>(p) = pack_bf16x8(f);
 }
 __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    st_f32x8(p, f);
+  } else {  // a tensor that starts 16 bytes into a sector
+    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+// The same from shared memory.  FP32: lanes 4..7 of every eight take their
+// upper 16 bytes first, so that eight lanes 32 bytes apart meet all the banks.
+__device__ __forceinline__ void load8_sh(const __nv_bfloat16 *p, float (&f)[8]) { load8(p, f); }
+__device__ __forceinline__ void load8_sh(const float *p, float (&f)[8]) {
+  const bool up = (threadIdx.x >> 2) & 1;
+  const float4 a = reinterpret_cast<const float4 *>(p)[up ? 1 : 0], b = reinterpret_cast<const float4 *>(p)[up ? 0 : 1];
+  f[0] = up ? b.x : a.x, f[1] = up ? b.y : a.y, f[2] = up ? b.z : a.z, f[3] = up ? b.w : a.w;
+  f[4] = up ? a.x : b.x, f[5] = up ? a.y : b.y, f[6] = up ? a.z : b.z, f[7] = up ? a.w : b.w;
 }
 // h rounded to the stream's type (the value later readers of h see)
 __device__ __forceinline__ void round8(const __nv_bfloat16 *, float (&f)[8]) {
@@ -76,16 +89,16 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
   return s;
 }
 
-// Codes of 8 values of a tile with scale S (see codes8 in quant.cu); a
-// non-finite S gives NaN codes.
+// Codes of 8 values of a tile with scale S.  y carries FP32 rounding already,
+// so y times the reciprocal of S (2 roundings) serves for the quotient; a tiny
+// S, whose reciprocal overflows, takes the division, and a NaN one gives NaN
+// codes.
 __device__ __forceinline__ uint2 tile_codes(const float (&f)[8], float S) {
   uint32_t lo = 0, hi = 0;
   if (S >= 0x1p-100f) {
     const float r = __frcp_rn(S);
-    lo = e4m3x2_rn_sat(div_by_recip(f[0], S, r), div_by_recip(f[1], S, r)) |
-         (e4m3x2_rn_sat(div_by_recip(f[2], S, r), div_by_recip(f[3], S, r)) << 16);
-    hi = e4m3x2_rn_sat(div_by_recip(f[4], S, r), div_by_recip(f[5], S, r)) |
-         (e4m3x2_rn_sat(div_by_recip(f[6], S, r), div_by_recip(f[7], S, r)) << 16);
+    lo = e4m3x2_rn_sat(f[0] * r, f[1] * r) | (e4m3x2_rn_sat(f[2] * r, f[3] * r) << 16);
+    hi = e4m3x2_rn_sat(f[4] * r, f[5] * r) | (e4m3x2_rn_sat(f[6] * r, f[7] * r) << 16);
   } else if (S != 0.0f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) lo |= static_cast<uint32_t>(e4m3_rn_sat(f[i] / S)) << (8 * i);
@@ -93,6 +106,23 @@ __device__ __forceinline__ uint2 tile_codes(const float (&f)[8], float S) {
     for (int i = 0; i < 4; ++i) hi |= static_cast<uint32_t>(e4m3_rn_sat(f[4 + i] / S)) << (8 * i);
   }
   return make_uint2(lo, hi);
+}
+
+// max(|a|, |b|), NaN if either is
+__device__ __forceinline__ float amax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// A 128-channel tile's scale from its 16 lanes' maxima; NaN where the tile
+// holds an infinity or a NaN.
+template <bool POW2>
+__device__ __forceinline__ float tile_scale(float am) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) am = amax_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+  if (!(am <= 3.402823466e38f)) return __uint_as_float(0x7FFFFFFFu);
+  return POW2 ? pow2_scale(am) : am / 448.0f;
 }
 
 struct NormFwd {
@@ -151,7 +181,7 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
     // a tile's 16 lanes are all inside or all outside the row
     const bool in = live && c < nch;
     if (in && p.h) store8(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k]);
-    uint32_t am = 0;
+    float am = 0.0f;
     if (in) {
       float w[8];
 #pragma unroll
@@ -160,16 +190,11 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         f[k][i] = f[k][i] * rstd * w[i];
-        // as integers, |NaN| > |inf| > every finite magnitude
-        am = max(am, __float_as_uint(f[k][i]) & 0x7FFFFFFFu);
+        am = amax_nan(am, f[k][i]);
       }
       if (p.y) store8(p.y + r * p.cols + c * 8, f[k]);
     }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-    const float amax = __uint_as_float(am);
-    float S = POW2 ? pow2_scale(amax) : amax / 448.0f;
-    if (am >= 0x7F800000u) S = __uint_as_float(0x7FFFFFFFu);
+    const float S = tile_scale<POW2>(am);
     if (in) {
       *reinterpret_cast<uint2 *>(p.q + r * p.cols + c * 8) = tile_codes(f[k], S);
       if ((threadIdx.x & 15) == 0) p.s[r * (p.cols / 128) + (c >> 4)] = S;
@@ -188,29 +213,25 @@ struct NormBwd {
 };
 }  // namespace
 
-template <typename TY, typename TS, typename TX, int CH, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_kernel(const NormBwd p) {
-  __shared__ float buf[2][8 * 32];
-  extern __shared__ float dw_sh[];  // [blockDim.y, cols] when a CTA holds several rows
+// Rows too long for the ring below: 4 chunks a thread, straight from memory.
+template <typename TY, typename TS, typename TX, int CH>
+__global__ void __launch_bounds__(1024, 1) add_rmsnorm_bwd_kernel(const NormBwd p) {
+  __shared__ float buf[2][32];
   const int nch = p.cols / 8;
   float dw[CH][8];
 #pragma unroll
   for (int k = 0; k < CH; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   int ph = 0;
-  // every thread of the CTA makes the same number of turns (row_sum is a CTA barrier)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, ph ^= 1) {
-    const int64_t r = r0 + threadIdx.y;
-    const bool live = r < p.rows;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, ph ^= 1) {
     float n[CH][8], g[CH][8];
     float sum = 0.0f;
-    const float rstd = live ? p.rstd[r] : 0.0f;
+    const float rstd = p.rstd[r];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
-      if (live && c < nch) {
+      if (c < nch) {
         load8(static_cast<const TS *>(p.h) + r * p.cols + c * 8, n[k]);
         load8(static_cast<const TY *>(p.dy) + r * p.cols + c * 8, g[k]);
         float w[8];
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_kernel(const NormBwd 
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
-      if (live && c < nch) {
+      if (c < nch) {
         float d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] = 0.0f;
@@ -243,26 +264,229 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_kernel(const NormBwd 
     }
   }
   if (!p.dw_part) return;
-  float *part = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.cols;
-  if (blockDim.y == 1) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = threadIdx.x + k * blockDim.x;
-      if (c < nch) store8(part + c * 8, dw[k]);
-    }
-    return;
-  }
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = threadIdx.x + k * blockDim.x;
-    if (c < nch) store8(dw_sh + threadIdx.y * p.cols + c * 8, dw[k]);
+    if (c < nch) store8(p.dw_part + static_cast<int64_t>(blockIdx.x) * p.cols + c * 8, dw[k]);
+  }
+}
+
+// ------------------------------------------------------ rows through a ring
+// For batches that give each CTA several rows: a CTA stays and takes rows
+// blockIdx.x, + gridDim.x, ...; one thread copies the next rows' inputs into a
+// ring of shared-memory stages (bulk copies, one per input) while the CTA works
+// on the current one.  Two 8-channel chunks per thread; the weight (and dw)
+// stay in registers from row to row.  One barrier per row, for the row's sum:
+// every thread has taken its inputs out of the stage by then, so the stage's
+// next copy starts right behind it.
+namespace {
+constexpr int kRing = 4;  // stages at most
+struct RingBars {
+  uint64_t full[kRing];
+  alignas(16) float red[2][32];
+  int abort_flag;
+};
+
+// Sum over the CTA: each warp's sum into `red`, one barrier, the warps' sums in
+// a fixed order.  red[nwarps..31] stay zero.
+__device__ __forceinline__ float ring_sum(float v, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); i += 4) {
+    const float4 q = *reinterpret_cast<const float4 *>(red + i);
+    s += (q.x + q.y) + (q.z + q.w);
+  }
+  return s;
+}
+
+__device__ __forceinline__ void ring_init(RingBars *b, int stages) {
+  if (threadIdx.x < 64) b->red[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+  if (blockDim.x < 64 && threadIdx.x < 32) b->red[1][threadIdx.x] = 0.0f;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&b->full[i], 1);
+    b->abort_flag = 0;
+    fence_mbar_init();
   }
   __syncthreads();
-  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.cols; c += blockDim.x * blockDim.y) {
-    float s = 0.0f;
-    for (int y = 0; y < static_cast<int>(blockDim.y); ++y) s += dw_sh[y * p.cols + c];
-    part[c] = s;
+}
+
+// Copies still in flight (only after a wait that gave up) land before the CTA
+// leaves.
+__device__ __forceinline__ void ring_drain(RingBars *b, int stages, uint32_t rows) {
+  if (threadIdx.x == 0 && b->abort_flag) {
+    int quiet = 0;
+    const WaitCtl drain{&quiet, nullptr, 100000000ull};
+    const uint32_t n = rows < static_cast<uint32_t>(stages) ? rows : stages;
+    for (uint32_t i = rows - n; i < rows; ++i) mbar_wait(&b->full[i % stages], (i / stages) & 1, drain);
   }
+  __syncthreads();
+}
+}  // namespace
+
+template <typename TS, bool POW2, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) add_rmsnorm_quant_ring_kernel(const NormFwd p, int stages) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) RingBars bars;
+  const int nch = p.cols / 8;
+  const uint32_t in_bytes = static_cast<uint32_t>(p.cols * sizeof(TS));
+  const uint32_t stage_bytes = p.resid ? 2 * in_bytes : in_bytes;
+  ring_init(&bars, stages);
+  const int64_t step = gridDim.x;
+  auto copy_in = [&](uint32_t i) {
+    const int64_t r = blockIdx.x + i * step;
+    if (r >= p.rows) return;
+    uint8_t *st = ring + (i % stages) * stage_bytes;
+    uint64_t *bar = &bars.full[i % stages];
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(st, static_cast<const TS *>(p.x) + r * p.ld_x, in_bytes, bar);
+    if (p.resid) bulk_load(st + in_bytes, static_cast<const TS *>(p.resid) + r * p.ld_r, in_bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages; ++i) copy_in(i);
+  float w[2][8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = threadIdx.x + k * blockDim.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[k][i] = 1.0f;
+    if (p.w && c < nch) load8(p.w + c * 8, w[k]);
+  }
+  const WaitCtl ctl{&bars.abort_flag, nullptr, kDefaultWaitLimitNs};
+  uint32_t it = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += step, ++it) {
+    const int s = it % stages;
+    const bool ok = mbar_wait(&bars.full[s], (it / stages) & 1, ctl);
+    const TS *x = reinterpret_cast<const TS *>(ring + s * stage_bytes);
+    float f[2][8], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = threadIdx.x + k * blockDim.x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[k][i] = 0.0f;
+      if (c < nch) {
+        load8_sh(x + c * 8, f[k]);
+        if (p.resid) {
+          float g[8];
+          load8_sh(x + p.cols + c * 8, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[k][i] += g[i];
+          round8(x, f[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[k][i], f[k][i], ss);
+      }
+    }
+    ss = ring_sum(ss, bars.red[it & 1]);
+    if (threadIdx.x == 0) copy_in(it + stages);
+    float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+    if (!ok) rstd = __uint_as_float(0x7FFFFFFFu);  // a copy that never arrived shows as NaN
+    if (threadIdx.x == 0 && p.rstd) p.rstd[r] = rstd;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = threadIdx.x + k * blockDim.x;
+      const bool in = c < nch;
+      if (in && p.h) store8(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k]);
+      float am = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[k][i] = f[k][i] * rstd * w[k][i];
+        if (in) am = amax_nan(am, f[k][i]);
+      }
+      if (in && p.y) store8(p.y + r * p.cols + c * 8, f[k]);
+      const float S = tile_scale<POW2>(am);
+      if (in) {
+        *reinterpret_cast<uint2 *>(p.q + r * p.cols + c * 8) = tile_codes(f[k], S);
+        if ((threadIdx.x & 15) == 0) p.s[r * (p.cols / 128) + (c >> 4)] = S;
+      }
+    }
+  }
+  ring_drain(&bars, stages, it);
+}
+
+template <typename TY, typename TS, typename TX, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int stages) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) RingBars bars;
+  const int nch = p.cols / 8;
+  const uint32_t y_bytes = static_cast<uint32_t>(p.cols * sizeof(TY)), s_bytes = static_cast<uint32_t>(p.cols * sizeof(TS));
+  const uint32_t stage_bytes = y_bytes + (p.dres ? 2 * s_bytes : s_bytes);
+  ring_init(&bars, stages);
+  const int64_t step = gridDim.x;
+  auto copy_in = [&](uint32_t i) {
+    const int64_t r = blockIdx.x + i * step;
+    if (r >= p.rows) return;
+    uint8_t *st = ring + (i % stages) * stage_bytes;
+    uint64_t *bar = &bars.full[i % stages];
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(st, static_cast<const TY *>(p.dy) + r * p.cols, y_bytes, bar);
+    bulk_load(st + y_bytes, static_cast<const TS *>(p.h) + r * p.cols, s_bytes, bar);
+    if (p.dres) bulk_load(st + y_bytes + s_bytes, static_cast<const TS *>(p.dres) + r * p.cols, s_bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages; ++i) copy_in(i);
+  float w[2][8], dw[2][8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = threadIdx.x + k * blockDim.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[k][i] = 1.0f;
+      dw[k][i] = 0.0f;
+    }
+    if (p.w && c < nch) load8(p.w + c * 8, w[k]);
+  }
+  const WaitCtl ctl{&bars.abort_flag, nullptr, kDefaultWaitLimitNs};
+  uint32_t it = 0;
+  float next = blockIdx.x < p.rows ? __ldg(p.rstd + blockIdx.x) : 0.0f;
+  for (int64_t r = blockIdx.x; r < p.rows; r += step, ++it) {
+    float rstd = next;
+    if (r + step < p.rows) next = __ldg(p.rstd + r + step);
+    const int s = it % stages;
+    // a copy that never arrived shows as NaN
+    if (!mbar_wait(&bars.full[s], (it / stages) & 1, ctl)) rstd = __uint_as_float(0x7FFFFFFFu);
+    const uint8_t *st = ring + s * stage_bytes;
+    float n[2][8], g[2][8], d[2][8], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = threadIdx.x + k * blockDim.x;
+      if (c < nch) {
+        load8_sh(reinterpret_cast<const TY *>(st) + c * 8, g[k]);
+        load8_sh(reinterpret_cast<const TS *>(st + y_bytes) + c * 8, n[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[k][i] = 0.0f;
+        if (p.dres) load8_sh(reinterpret_cast<const TS *>(st + y_bytes + s_bytes) + c * 8, d[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          n[k][i] *= rstd;
+          dw[k][i] = fmaf(g[k][i], n[k][i], dw[k][i]);
+          g[k][i] *= w[k][i];
+          sum = fmaf(g[k][i], n[k][i], sum);
+        }
+      }
+    }
+    const float m = ring_sum(sum, bars.red[it & 1]) / static_cast<float>(p.cols);
+    if (threadIdx.x == 0) copy_in(it + stages);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = threadIdx.x + k * blockDim.x;
+      if (c < nch) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[k][i] = fmaf(rstd, fmaf(-n[k][i], m, g[k][i]), d[k][i]);
+        store8(static_cast<TX *>(p.dx) + r * p.cols + c * 8, d[k]);
+      }
+    }
+  }
+  if (p.dw_part) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = threadIdx.x + k * blockDim.x;
+      if (c < nch) store8(p.dw_part + static_cast<int64_t>(blockIdx.x) * p.cols + c * 8, dw[k]);
+    }
+  }
+  ring_drain(&bars, stages, it);
 }
 
 // dw[c] = sum over the parts, 32 columns per CTA: each of 32 warps takes every
@@ -295,29 +519,106 @@ inline dim3 norm_block(int cols, int ch) {
   return dim3(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
 }
 
-// Rows of up to 8192 channels take at most 256 threads, which leaves the
-// registers for CH = 4 chunks a thread; longer rows take up to 1024.
-constexpr int kCh = 4;
+constexpr int kMaxCtas = 8;  // per SM
+constexpr int kSmemPerSM = 233472 - 1024;  // shared memory of an SM, less one CTA's reserve
 
-template <typename TS, bool POW2>
-cudaError_t launch_norm_fwd(const NormFwd &p, cudaStream_t st) {
-  const dim3 b = norm_block(p.cols, kCh);
+// How a ring kernel goes over `rows` rows of `row_bytes` inputs: threads, CTAs
+// per SM, stages; ok = false where two stages do not fit or a thread would hold
+// more than two chunks.
+struct RingPlan {
+  bool ok;
+  int threads, per_sm, stages;
+  int smem;
+  int64_t grid;
+};
+// `threads_per_sm`: as many as the kernel's registers allow.
+inline RingPlan ring_plan(int64_t rows, int cols, int64_t row_bytes, int threads_per_sm) {
+  RingPlan p{};
+  p.threads = (cols / 16 + 31) / 32 * 32;
+  if (p.threads > 1024) return p;
+  int per_sm = threads_per_sm / p.threads;
+  if (per_sm > kMaxCtas) per_sm = kMaxCtas;
+  if (per_sm < 1) per_sm = 1;
+  // fewer CTAs, if that is what two stages take
+  while (per_sm > 1 && (2 * row_bytes + 1536) * per_sm > kSmemPerSM) --per_sm;
+  int64_t st = (kSmemPerSM / per_sm - 1536) / row_bytes;
+  if (st > kRing) st = kRing;
+  if (st < 2) return p;
+  p.ok = true;
+  p.per_sm = per_sm;
+  p.stages = static_cast<int>(st);
+  p.smem = static_cast<int>(st * row_bytes);
+  const int64_t most = static_cast<int64_t>(moe_host::sm_count()) * per_sm;
+  p.grid = rows < most ? rows : most;
+  return p;
+}
+
+template <typename TS, int CH, bool POW2>
+cudaError_t launch_norm_rows(const NormFwd &p, cudaStream_t st) {
+  const dim3 b = norm_block(p.cols, CH);
   const unsigned grid = static_cast<unsigned>((p.rows + b.y - 1) / b.y);
-  if (b.x <= 256)
-    add_rmsnorm_quant_kernel<TS, kCh, POW2, 256><<<grid, b, 0, st>>>(p);
+  if (b.x * b.y <= 256)
+    add_rmsnorm_quant_kernel<TS, CH, POW2, 256><<<grid, b, 0, st>>>(p);
   else
-    add_rmsnorm_quant_kernel<TS, kCh, POW2, 1024><<<grid, b, 0, st>>>(p);
+    add_rmsnorm_quant_kernel<TS, CH, POW2, 1024><<<grid, b, 0, st>>>(p);
   return cudaGetLastError();
 }
 
+template <typename TS, bool POW2>
+cudaError_t launch_norm_fwd(const NormFwd &p, cudaStream_t st) {
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * sizeof(TS) * (p.resid ? 2 : 1);
+  const RingPlan pl = ring_plan(p.rows, p.cols, row_bytes, 1024);
+  if (pl.ok && p.rows >= 2 * pl.grid) {
+    if (pl.threads <= 512) {
+      static std::atomic<uint64_t> done{0};
+      if (const cudaError_t e = smem_attr_once(add_rmsnorm_quant_ring_kernel<TS, POW2, 512, 2>, kSmemPerSM - 1536, done))
+        return e;
+      add_rmsnorm_quant_ring_kernel<TS, POW2, 512, 2>
+          <<<static_cast<unsigned>(pl.grid), pl.threads, pl.smem, st>>>(p, pl.stages);
+    } else {
+      static std::atomic<uint64_t> done{0};
+      if (const cudaError_t e = smem_attr_once(add_rmsnorm_quant_ring_kernel<TS, POW2, 1024, 1>, kSmemPerSM - 1536, done))
+        return e;
+      add_rmsnorm_quant_ring_kernel<TS, POW2, 1024, 1>
+          <<<static_cast<unsigned>(pl.grid), pl.threads, pl.smem, st>>>(p, pl.stages);
+    }
+    return cudaGetLastError();
+  }
+  // A row or two per CTA: as many threads as the row has chunks, up to 1024
+  // (one token, 7168 channels: 8 us with one chunk a thread, 12 with four).
+  return p.cols <= 8192 ? launch_norm_rows<TS, 1, POW2>(p, st) : launch_norm_rows<TS, 4, POW2>(p, st);
+}
+
+template <typename TY, typename TS>
+int64_t bwd_row_bytes(int cols, bool dres) {
+  return static_cast<int64_t>(cols) * (sizeof(TY) + sizeof(TS) * (dres ? 2 : 1));
+}
+constexpr int kCh = 4;  // chunks a thread in the rows kernel
+
 template <typename TY, typename TS, typename TX>
-cudaError_t launch_norm_bwd(const NormBwd &p, int grid, cudaStream_t st) {
-  const dim3 b = norm_block(p.cols, kCh);
-  const size_t sh = b.y > 1 ? static_cast<size_t>(b.y) * p.cols * 4 : 0;  // 32 KB at most
-  if (b.x <= 256)
-    add_rmsnorm_bwd_kernel<TY, TS, TX, kCh, 256><<<grid, b, sh, st>>>(p);
-  else
-    add_rmsnorm_bwd_kernel<TY, TS, TX, kCh, 1024><<<grid, b, sh, st>>>(p);
+cudaError_t launch_norm_bwd(const NormBwd &p, int *parts, cudaStream_t st) {
+  const RingPlan pl = ring_plan(p.rows, p.cols, bwd_row_bytes<TY, TS>(p.cols, p.dres != nullptr), 512);
+  if (pl.ok) {
+    *parts = static_cast<int>(pl.grid);
+    if (pl.threads <= 512) {
+      static std::atomic<uint64_t> done{0};
+      if (const cudaError_t e = smem_attr_once(add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 512>, kSmemPerSM - 1536, done))
+        return e;
+      add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 512>
+          <<<static_cast<unsigned>(pl.grid), pl.threads, pl.smem, st>>>(p, pl.stages);
+    } else {
+      static std::atomic<uint64_t> done{0};
+      if (const cudaError_t e = smem_attr_once(add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 1024>, kSmemPerSM - 1536, done))
+        return e;
+      add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 1024>
+          <<<static_cast<unsigned>(pl.grid), pl.threads, pl.smem, st>>>(p, pl.stages);
+    }
+    return cudaGetLastError();
+  }
+  // rows too long for two stages of the ring (above about 9000 FP32 channels)
+  const int64_t most = 2 * static_cast<int64_t>(moe_host::sm_count());
+  *parts = static_cast<int>(p.rows < most ? p.rows : most);
+  add_rmsnorm_bwd_kernel<TY, TS, TX, kCh><<<*parts, norm_block(p.cols, kCh), 0, st>>>(p);
   return cudaGetLastError();
 }
 }  // namespace
@@ -332,11 +633,10 @@ cudaError_t launch_add_rmsnorm_quant(const void *x, int64_t ld_x, const void *re
              : (pow2 ? launch_norm_fwd<B, true>(p, st) : launch_norm_fwd<B, false>(p, st));
 }
 
-int norm_bwd_parts(int64_t rows, int cols) {
-  const dim3 b = norm_block(cols, kCh);
-  const int64_t want = (rows + b.y - 1) / b.y;
-  const int64_t most = 2 * static_cast<int64_t>(moe_host::sm_count());
-  return static_cast<int>(want < most ? want : most);
+// An upper bound on the CTAs of either backward kernel.
+int norm_bwd_parts(int64_t rows, int) {
+  const int64_t most = kMaxCtas * static_cast<int64_t>(moe_host::sm_count());
+  return static_cast<int>(rows < most ? rows : most);
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const void *dy, bool dy_f32, const void *h, const void *dres, bool f32,
@@ -344,17 +644,17 @@ cudaError_t launch_add_rmsnorm_bwd(const void *dy, bool dy_f32, const void *h, c
                                    float *dw, float *part, cudaStream_t st) {
   if (rows == 0) return dw ? cudaMemsetAsync(dw, 0, sizeof(float) * cols, st) : cudaSuccess;
   const NormBwd p{dy, h, dres, w, rstd, rows, cols, dx, dw ? part : nullptr};
-  const int grid = norm_bwd_parts(rows, cols);
+  int n = 0;
   using B = __nv_bfloat16;
   cudaError_t e;
   if (dy_f32)
-    e = f32 ? (dx_f32 ? launch_norm_bwd<float, float, float>(p, grid, st) : launch_norm_bwd<float, float, B>(p, grid, st))
-            : (dx_f32 ? launch_norm_bwd<float, B, float>(p, grid, st) : launch_norm_bwd<float, B, B>(p, grid, st));
+    e = f32 ? (dx_f32 ? launch_norm_bwd<float, float, float>(p, &n, st) : launch_norm_bwd<float, float, B>(p, &n, st))
+            : (dx_f32 ? launch_norm_bwd<float, B, float>(p, &n, st) : launch_norm_bwd<float, B, B>(p, &n, st));
   else
-    e = f32 ? (dx_f32 ? launch_norm_bwd<B, float, float>(p, grid, st) : launch_norm_bwd<B, float, B>(p, grid, st))
-            : (dx_f32 ? launch_norm_bwd<B, B, float>(p, grid, st) : launch_norm_bwd<B, B, B>(p, grid, st));
+    e = f32 ? (dx_f32 ? launch_norm_bwd<B, float, float>(p, &n, st) : launch_norm_bwd<B, float, B>(p, &n, st))
+            : (dx_f32 ? launch_norm_bwd<B, B, float>(p, &n, st) : launch_norm_bwd<B, B, B>(p, &n, st));
   if (e != cudaSuccess || !dw) return e;
-  norm_dw_join_kernel<<<cols / 32, 1024, 0, st>>>(part, grid, cols, dw);
+  norm_dw_join_kernel<<<cols / 32, 1024, 0, st>>>(part, n, cols, dw);
   return cudaGetLastError();
 }
 

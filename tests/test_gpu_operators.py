@@ -71,7 +71,7 @@ def check_norm(m, x, resid, w, pow2, out):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H", [(1, 128), (1, 7168), (3, 384), (37, 512), (64, 7168), (5, 1152), (2, 8320), (2, 32768),
-                                 (513, 1024)])
+                                 (513, 1024), (1300, 7168), (700, 16384), (5001, 128)])
 def test_norm_forward(m, T, H, dtype):
     for k, (resid, pow2, weight) in enumerate([(True, False, True), (False, True, True), (True, True, False)]):
         x, r, w = norm_inputs(T, H, dtype, resid, T + H + k)
@@ -98,6 +98,27 @@ def test_norm_forward_strided_in_place_and_guarded(m):
         assert torch.equal(a, b)
 
 
+def test_norm_sixteen_byte_aligned_buffers(m):
+    """Tensors that start 16 bytes into a 32-byte sector, and enough rows for every CTA to take several."""
+    T, H = 2500, 256
+
+    def off(dtype, src=None):
+        n = 16 // torch.empty((), dtype=dtype).element_size()
+        t = torch.empty(T * H + n, dtype=dtype, device="cuda")[n:].view(T, H)
+        assert t.data_ptr() % 32 == 16
+        return t if src is None else t.copy_(src)
+
+    for dtype in (torch.bfloat16, torch.float32):
+        x, r, w = norm_inputs(T, H, dtype, True, 11)
+        h, y = off(dtype), off(torch.bfloat16)
+        out = m.fp8_add_rmsnorm_quant_1x128(off(dtype, x), off(dtype, r), w, EPS, h=h, y=y)
+        check_norm(m, x, r, w, False, out)
+        dy = torch.randn((T, H), generator=torch.Generator().manual_seed(1)).cuda()
+        want = m.add_rmsnorm_backward(dy, h.clone(), out[4], w, dres=r, dx_dtype=torch.float32)
+        got = m.add_rmsnorm_backward(off(torch.float32, dy), h, out[4], w, dres=off(dtype, r), dx=off(torch.float32))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_norm_forward_zero_and_nonfinite_rows(m):
     x, _, w = norm_inputs(4, 512, torch.bfloat16, False, 5)
     x = x.contiguous()
@@ -118,7 +139,7 @@ def test_norm_forward_zero_and_nonfinite_rows(m):
 @pytest.mark.parametrize("dy_t,h_t,dx_t", [(a, b, c) for a in (torch.bfloat16, torch.float32)
                                            for b in (torch.bfloat16, torch.float32)
                                            for c in (torch.bfloat16, torch.float32)])
-@pytest.mark.parametrize("T,H", [(1, 128), (9, 384), (300, 7168), (1300, 512), (3, 32768), (2, 8320)])
+@pytest.mark.parametrize("T,H", [(1, 128), (9, 384), (300, 7168), (1300, 512), (3, 32768), (2, 8320), (310, 12288), (5000, 128)])
 def test_norm_backward(m, T, H, dy_t, h_t, dx_t):
     g = torch.Generator().manual_seed(T + H)
     h = (torch.randn((T, H), generator=g) * 2).to(h_t).cuda()
