@@ -421,43 +421,71 @@ def moe_backward(cfg: MoeConfig, w: dict, wt: dict, x, dout, fwd_ws, dx=None, dW
 
 
 # ------------------------------------------- norm, balance loss, router
-def _want(where: str, t, name: str, dtype, shape, device=None, contiguous=True) -> None:
-    """Raise MoeError(MOE_ERR_INVALID_ARG) unless t is a tensor of that type
-    and shape (None: any) on that CUDA device."""
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda
-            or (device is not None and t.device != device) or (shape is not None and t.shape != shape)
-            or (contiguous and not t.is_contiguous())):
-        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is {got}, wanted "
-                       f"{'/'.join(str(d) for d in dtypes)}{'' if shape is None else ' ' + str(tuple(shape))}"
-                       f"{' contiguous' if contiguous else ''} on {device or 'a CUDA device'}")
+# These calls check every tensor they are given (type, shape, device, strides)
+# and raise MoeError(MOE_ERR_INVALID_ARG) otherwise.  A decode step makes them
+# back to back, so the checks are written to cost little: one test per
+# property, the message only put together on the way out.
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
-class _on:
-    """Make `device` current for a call (the library launches on the current
-    device) and give the call's stream: the caller's, or that device's
-    current one."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guard = device, stream, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _refuse(where: str, what: str):
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-_STREAM_TYPES = (torch.bfloat16, torch.float32)
+def _want(where: str, t, name: str, dtype, shape, idx: int) -> int:
+    """t's device pointer; t is a contiguous `dtype` tensor of that shape
+    (None: any) on CUDA device `idx`."""
+    try:
+        if t.dtype is dtype and t.get_device() == idx and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+    _refuse(where, f"{name} is {got}, wanted a contiguous {dtype}{'' if shape is None else ' ' + str(tuple(shape))} "
+                   f"on CUDA device {idx}")
 
 
-def _code(dtype) -> int:
-    return MOE_DTYPE_F32 if dtype == torch.float32 else MOE_DTYPE_BF16
+def _stream_type(where: str, t, name: str) -> int:
+    """MOE_DTYPE_* of a bf16 or float32 tensor."""
+    dt = getattr(t, "dtype", None)
+    if dt is _BF16:
+        return MOE_DTYPE_BF16
+    if dt is not _F32:
+        _refuse(where, f"{name} is {dt or type(t).__name__}, wanted bf16 or float32")
+    return MOE_DTYPE_F32
+
+
+def _cuda_index(where: str, t, name: str) -> int:
+    idx = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if idx < 0:
+        _refuse(where, f"{name} is not on a CUDA device")
+    return idx
+
+
+def _on_device(fn, idx: int, stream, where: str, args) -> None:
+    """fn(*args, stream) with device `idx` current (the library launches on
+    the current device), on the caller's stream or that device's current one."""
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(idx)
+    else:
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if idx == torch._C._cuda_getDevice():
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(idx):
+            status = fn(*args, st)
+    if status != MOE_OK:
+        raise MoeError(status, where)
+
+
+def _scratch(fn, idx: int, *args) -> torch.Tensor:
+    """A workspace of fn(*args) bytes, the size being the current device's."""
+    if idx == torch._C._cuda_getDevice():
+        n = fn(*args)
+    else:
+        with torch.cuda.device(idx):
+            n = fn(*args)
+    return torch.empty(n if n > 256 else 256, dtype=_U8, device=torch.device("cuda", idx))
 
 
 def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: float = 1e-6, h=None, y=None, q=None,
@@ -467,36 +495,40 @@ def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: f
     weight: float32 [cols] or None.  Returns (h, y bf16, q uint8, scales,
     rstd); without resid, h is x unless a buffer is given."""
     where = "fp8_add_rmsnorm_quant_1x128"
-    _want(where, x, "x", _STREAM_TYPES, None, contiguous=False)
-    if x.dim() != 2 or (x.numel() and x.stride(1) != 1):
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: x is [rows, cols] with unit stride along cols")
-    dev, shape = x.device, x.shape
+    code, idx = _stream_type(where, x, "x"), _cuda_index(where, x, "x")
+    shape = x.shape
+    if len(shape) != 2 or (shape[1] > 1 and x.stride(1) != 1):
+        _refuse(where, "x is [rows, cols] with unit stride along cols")
     rows, cols = shape
-    if resid is not None:
-        _want(where, resid, "resid", x.dtype, shape, dev, contiguous=False)
-        if resid.numel() and resid.stride(1) != 1:
-            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: resid has unit stride along cols")
-        h = torch.empty(shape, dtype=x.dtype, device=dev) if h is None else h
-    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if y is None else y
-    q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
-    sshape = (rows, cols // 128)
-    scales = torch.empty(sshape, dtype=torch.float32, device=dev) if scales is None else scales
-    rstd = torch.empty((rows,), dtype=torch.float32, device=dev) if rstd is None else rstd
-    if weight is not None:
-        _want(where, weight, "weight", torch.float32, (cols,), dev)
-    if h is not None:
-        _want(where, h, "h", x.dtype, shape, dev)
-    _want(where, y, "y", torch.bfloat16, shape, dev)
-    _want(where, q, "q", torch.uint8, shape, dev)
-    _want(where, scales, "scales", torch.float32, sshape, dev)
-    _want(where, rstd, "rstd", torch.float32, (rows,), dev)
+    dtype, dev = x.dtype, x.device
     # a single row has no row stride
-    ld = x.stride(0) if rows > 1 else cols
-    ldr = cols if resid is None or rows <= 1 else resid.stride(0)
-    with _on(dev, stream) as st:
-        _check(lib.fp8_add_rmsnorm_quant_1x128(_ptr(x), ld, _ptr(resid), ldr, _code(x.dtype), _ptr(weight), eps, rows,
-                                               cols, _ptr(h), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd),
-                                               MOE_SCALE_POW2 if pow2 else MOE_SCALE_AMAX, st), where)
+    ld = ldr = cols
+    if rows > 1:
+        ld = x.stride(0)
+    rp = None
+    if resid is not None:
+        if (not isinstance(resid, torch.Tensor) or resid.dtype is not dtype or resid.get_device() != idx
+                or resid.shape != shape or (cols > 1 and resid.stride(1) != 1)):
+            _refuse(where, f"resid is not {dtype} {tuple(shape)} with unit stride along cols on CUDA device {idx}")
+        if rows > 1:
+            ldr = resid.stride(0)
+        rp = resid.data_ptr()
+        if h is None:
+            h = torch.empty(shape, dtype=dtype, device=dev)
+    if y is None:
+        y = torch.empty(shape, dtype=_BF16, device=dev)
+    if q is None:
+        q = torch.empty(shape, dtype=_U8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, cols // 128), dtype=_F32, device=dev)
+    if rstd is None:
+        rstd = torch.empty((rows,), dtype=_F32, device=dev)
+    _on_device(lib.fp8_add_rmsnorm_quant_1x128, idx, stream, where, (
+        x.data_ptr(), ld, rp, ldr, code, None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
+        eps, rows, cols, None if h is None else _want(where, h, "h", dtype, shape, idx),
+        _want(where, y, "y", _BF16, shape, idx), _want(where, q, "q", _U8, shape, idx),
+        _want(where, scales, "scales", _F32, (rows, cols // 128), idx), _want(where, rstd, "rstd", _F32, (rows,), idx),
+        MOE_SCALE_POW2 if pow2 else MOE_SCALE_AMAX))
     return x if h is None else h, y, q, scales, rstd
 
 
@@ -506,29 +538,27 @@ def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, 
     rstd: the forward's; dres: gradient reaching h past the norm, of h's type.
     dx (the gradient of x and of resid) has dx_dtype, by default h's type."""
     where = "add_rmsnorm_backward"
-    _want(where, h, "h", _STREAM_TYPES, None)
-    if h.dim() != 2:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: h is [rows, cols]")
-    dev, shape = h.device, h.shape
+    code, idx = _stream_type(where, h, "h"), _cuda_index(where, h, "h")
+    shape, dtype = h.shape, h.dtype
+    if len(shape) != 2:
+        _refuse(where, "h is [rows, cols]")
     rows, cols = shape
-    _want(where, dy, "dy", _STREAM_TYPES, shape, dev)
-    _want(where, rstd, "rstd", torch.float32, (rows,), dev)
-    if weight is not None:
-        _want(where, weight, "weight", torch.float32, (cols,), dev)
-    if dres is not None:
-        _want(where, dres, "dres", h.dtype, shape, dev)
-    dx = torch.empty(shape, dtype=dx_dtype or h.dtype, device=dev) if dx is None else dx
-    _want(where, dx, "dx", _STREAM_TYPES if dx_dtype is None else dx_dtype, shape, dev)
-    dw = torch.empty((cols,), dtype=torch.float32, device=dev) if dw is None else dw
-    _want(where, dw, "dw", torch.float32, (cols,), dev)
-    with _on(dev, stream) as st:
-        if ws is None:
-            ws = torch.empty(max(int(lib.add_rmsnorm_backward_workspace_size(rows, cols)), 256), dtype=torch.uint8,
-                             device=dev)
-        _want(where, ws, "ws", torch.uint8, None, dev)
-        _check(lib.add_rmsnorm_backward(_ptr(dy), _code(dy.dtype), _ptr(h), _ptr(dres), _code(h.dtype), _ptr(weight),
-                                        _ptr(rstd), rows, cols, _ptr(dx), _code(dx.dtype), _ptr(dw), _ptr(ws),
-                                        ws.numel(), st), where)
+    ycode = _stream_type(where, dy, "dy")
+    if dx is None:
+        dx = torch.empty(shape, dtype=dx_dtype or dtype, device=h.device)
+    elif dx_dtype is not None and dx.dtype is not dx_dtype:
+        _refuse(where, f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+    xcode = _stream_type(where, dx, "dx")
+    if dw is None:
+        dw = torch.empty((cols,), dtype=_F32, device=h.device)
+    if ws is None:
+        ws = _scratch(lib.add_rmsnorm_backward_workspace_size, idx, rows, cols)
+    _on_device(lib.add_rmsnorm_backward, idx, stream, where, (
+        _want(where, dy, "dy", dy.dtype, shape, idx), ycode, _want(where, h, "h", dtype, shape, idx),
+        None if dres is None else _want(where, dres, "dres", dtype, shape, idx), code,
+        None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
+        _want(where, rstd, "rstd", _F32, (rows,), idx), rows, cols, _want(where, dx, "dx", dx.dtype, shape, idx), xcode,
+        _want(where, dw, "dw", _F32, (cols,), idx), _want(where, ws, "ws", _U8, None, idx), ws.numel()))
     return dx, dw
 
 
@@ -547,13 +577,23 @@ def moe_route_logits(cfg: MoeConfig, T: int, ws: torch.Tensor) -> torch.Tensor:
     return ws[:n * T * cfg.n_routed * 4].view(torch.float32).view(n, T, cfg.n_routed)
 
 
-def _router_state(where: str, cfg: MoeConfig, logits, idx):
-    _want(where, logits, "logits", torch.float32, None)
-    if logits.dim() != 3 or logits.shape[0] < 1 or logits.shape[2] != cfg.n_routed:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: logits is [n_splits, T, {cfg.n_routed}]")
-    n, T, _ = logits.shape
-    _want(where, idx, "idx", torch.int32, (T, cfg.top_k), logits.device)
-    return n, T, logits.device
+def _router_state(where: str, cfg: MoeConfig, logits, picks):
+    """(n_splits, T, device, logits pointer, picks pointer)"""
+    idx = _cuda_index(where, logits, "logits")
+    shape = logits.shape
+    if len(shape) != 3 or shape[0] < 1 or shape[2] != cfg.n_routed:
+        _refuse(where, f"logits is {tuple(shape)}, wanted [n_splits, T, {cfg.n_routed}]")
+    return (shape[0], shape[1], idx, _want(where, logits, "logits", _F32, None, idx),
+            _want(where, picks, "idx", _I32, (shape[1], cfg.top_k), idx))
+
+
+def _sequences(where: str, off, idx: int):
+    """(n_seq, pointer) of the offsets of packed sequences."""
+    p = _want(where, off, "seq_offsets", _I32, None, idx)
+    shape = off.shape
+    if len(shape) != 1 or shape[0] < 1:
+        _refuse(where, "seq_offsets is [n_seq + 1]")
+    return shape[0] - 1, p
 
 
 def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e-4, loss=None, counts=None, ws=None,
@@ -563,37 +603,30 @@ def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e
     N_r] (moe_route_logits, or the caller's own with n_splits = 1); idx: the
     picks; seq_offsets: int32 [n_seq + 1]."""
     where = "moe_balance_loss"
-    n, T, dev = _router_state(where, cfg, logits, idx)
-    _want(where, seq_offsets, "seq_offsets", torch.int32, None, dev)
-    if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: seq_offsets is [n_seq + 1]")
-    n_seq = seq_offsets.numel() - 1
-    loss = torch.empty((n_seq,), dtype=torch.float32, device=dev) if loss is None else loss
-    counts = torch.empty((n_seq, cfg.n_routed), dtype=torch.int32, device=dev) if counts is None else counts
-    _want(where, loss, "loss", torch.float32, (n_seq,), dev)
-    _want(where, counts, "counts", torch.int32, (n_seq, cfg.n_routed), dev)
-    with _on(dev, stream) as st:
-        if ws is None:
-            ws = torch.empty(max(int(lib.moe_balance_loss_workspace_size(C.byref(cfg), T, n_seq)), 256),
-                             dtype=torch.uint8, device=dev)
-        _want(where, ws, "ws", torch.uint8, None, dev)
-        err = new_err_flag(dev) if err is None else err
-        _want(where, err, "err", torch.int32, None, dev)
-        _check(lib.moe_balance_loss(C.byref(cfg), _ptr(logits), n, _ptr(idx), T, _ptr(seq_offsets), n_seq, alpha,
-                                    _ptr(loss), _ptr(counts), _ptr(ws), ws.numel(), _ptr(err), st), where)
+    n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
+    n_seq, op = _sequences(where, seq_offsets, dev)
+    if loss is None:
+        loss = torch.empty((n_seq,), dtype=_F32, device=logits.device)
+    if counts is None:
+        counts = torch.empty((n_seq, cfg.n_routed), dtype=_I32, device=logits.device)
+    cp = C.byref(cfg)
+    if ws is None:
+        ws = _scratch(lib.moe_balance_loss_workspace_size, dev, cp, T, n_seq)
+    if err is None:
+        err = new_err_flag(logits.device)
+    _on_device(lib.moe_balance_loss, dev, stream, where, (
+        cp, zp, n, ip, T, op, n_seq, alpha, _want(where, loss, "loss", _F32, (n_seq,), dev),
+        _want(where, counts, "counts", _I32, (n_seq, cfg.n_routed), dev), _want(where, ws, "ws", _U8, None, dev),
+        ws.numel(), _want(where, err, "err", _I32, None, dev)))
     return loss, counts
 
 
-def _balance_struct(where: str, cfg: MoeConfig, b: dict, dev) -> MoeBalanceGrad:
-    off, counts, dloss = b["seq_offsets"], b["counts"], b.get("dloss")
-    _want(where, off, "seq_offsets", torch.int32, None, dev)
-    if off.dim() != 1 or off.numel() < 1:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: seq_offsets is [n_seq + 1]")
-    n_seq = off.numel() - 1
-    _want(where, counts, "counts", torch.int32, (n_seq, cfg.n_routed), dev)
-    if dloss is not None:
-        _want(where, dloss, "dloss", torch.float32, (n_seq,), dev)
-    return MoeBalanceGrad(_ptr(off), n_seq, b.get("alpha", 1e-4), _ptr(counts), _ptr(dloss))
+def _balance_struct(where: str, cfg: MoeConfig, b: dict, idx: int) -> MoeBalanceGrad:
+    n_seq, op = _sequences(where, b["seq_offsets"], idx)
+    dloss = b.get("dloss")
+    return MoeBalanceGrad(op, n_seq, b.get("alpha", 1e-4),
+                          _want(where, b["counts"], "counts", _I32, (n_seq, cfg.n_routed), idx),
+                          None if dloss is None else _want(where, dloss, "dloss", _F32, (n_seq,), idx))
 
 
 def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None, balance=None, dlogits=None, dx=None,
@@ -605,37 +638,33 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
     counts, dloss (None: ones), alpha) of the balance loss; x bf16 [T, H] for
     dwr, wr bf16 [N_r, H] for dx.  dx_accumulate adds to dx."""
     where = "moe_router_backward"
-    n, T, dev = _router_state(where, cfg, logits, idx)
+    n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
     H, Nr = cfg.hidden, cfg.n_routed
+    if dx_accumulate and (dx is None or dx is True or dx is False):
+        _refuse(where, "dx_accumulate needs a dx to add to")
 
     def out(t, name, shape):
         if t is None or t is False:
-            return None
-        t = torch.empty(shape, dtype=torch.float32, device=dev) if t is True else t
-        _want(where, t, name, torch.float32, shape, dev)
-        return t
+            return None, None
+        if t is True:
+            t = torch.empty(shape, dtype=_F32, device=logits.device)
+        return t, _want(where, t, name, _F32, shape, dev)
 
-    if dx_accumulate and not isinstance(dx, torch.Tensor):
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: dx_accumulate needs a dx to add to")
-    dlogits, dx, dwr = out(dlogits, "dlogits", (T, Nr)), out(dx, "dx", (T, H)), out(dwr, "dwr", (Nr, H))
-    if dgate is not None:
-        _want(where, dgate, "dgate", torch.float32, (T, cfg.top_k), dev)
-    if x is not None or dwr is not None:
-        _want(where, x, "x", torch.bfloat16, (T, H), dev)
-    if wr is not None or dx is not None:
-        _want(where, wr, "wr", torch.bfloat16, (Nr, H), dev)
-    bal = None if balance is None else C.byref(_balance_struct(where, cfg, balance, dev))
-    with _on(dev, stream) as st:
-        if ws is None and (dx is not None or dwr is not None):
-            ws = torch.empty(max(int(lib.moe_router_backward_workspace_size(C.byref(cfg), T)), 256),
-                             dtype=torch.uint8, device=dev)
-        if ws is not None:
-            _want(where, ws, "ws", torch.uint8, None, dev)
-        err = new_err_flag(dev) if err is None else err
-        _want(where, err, "err", torch.int32, None, dev)
-        _check(lib.moe_router_backward(C.byref(cfg), _ptr(logits), n, _ptr(idx), T, _ptr(dgate), bal, _ptr(x), _ptr(wr),
-                                       _ptr(dlogits), _ptr(dx), int(dx_accumulate), _ptr(dwr), _ptr(ws),
-                                       0 if ws is None else ws.numel(), _ptr(err), st), where)
+    dlogits, lp = out(dlogits, "dlogits", (T, Nr))
+    dx, xp = out(dx, "dx", (T, H))
+    dwr, wp = out(dwr, "dwr", (Nr, H))
+    cp = C.byref(cfg)
+    if ws is None and (dx is not None or dwr is not None):
+        ws = _scratch(lib.moe_router_backward_workspace_size, dev, cp, T)
+    if err is None:
+        err = new_err_flag(logits.device)
+    _on_device(lib.moe_router_backward, dev, stream, where, (
+        cp, zp, n, ip, T, None if dgate is None else _want(where, dgate, "dgate", _F32, (T, cfg.top_k), dev),
+        None if balance is None else C.byref(_balance_struct(where, cfg, balance, dev)),
+        None if x is None and dwr is None else _want(where, x, "x", _BF16, (T, H), dev),
+        None if wr is None and dx is None else _want(where, wr, "wr", _BF16, (Nr, H), dev), lp, xp,
+        1 if dx_accumulate else 0, wp, None if ws is None else _want(where, ws, "ws", _U8, None, dev),
+        0 if ws is None else ws.numel(), _want(where, err, "err", _I32, None, dev)))
     return dlogits, dx, dwr
 
 

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "operators.cuh"
 
 namespace moe_host {
 

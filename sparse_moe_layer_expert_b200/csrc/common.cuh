@@ -418,13 +418,6 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Eight consecutive floats, one 32-byte sector (p 32-byte aligned).
-__device__ __forceinline__ void st_f32x8(float *p, const float *v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 // a / b rounded to nearest from y = RN(1/b): q0 = RN(a*y), the exact residual
 // r = a - b*q0 (one FMA), then RN(q0 + r*y).  One residual correction of the
 // quotient (Markstein's division by reciprocal, as presented in Muller et al.,
@@ -499,9 +492,5 @@ __device__ __forceinline__ uint8_t e4m3_rn_sat(float v) {
 namespace moe_host {
 int encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                    uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
-// Any rank up to 5: dims, strides (bytes, rank - 1 of them) and box innermost
-// first; 128-byte swizzle, zeros out of bounds.
-int encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int rank, const uint64_t *dims,
-                const uint64_t *strides, const uint32_t *box);
 int sm_count();
 }  // namespace moe_host

@@ -17,6 +17,7 @@
 // CTA order by a second kernel: no atomics, the same result on every run.
 #include "common.cuh"
 #include "kernels.h"
+#include "operators.cuh"
 
 namespace moe {
 

@@ -29,6 +29,7 @@
 //   dwr_join_kernel    adds the token ranges' partial sums in range order
 #include "common.cuh"
 #include "kernels.h"
+#include "operators.cuh"
 #include "router_math.cuh"
 
 namespace moe {
