@@ -226,7 +226,6 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
 // single CTA's 128 x 256 tile) and the operands' arrival fits beside it.
 namespace {
 constexpr int kParts = 3;
-constexpr int RP_THREADS = 384;  // warp 0 TMA, warp 1 MMA (even CTA), warps 4..11 epilogue
 
 __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
@@ -236,13 +235,6 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
-               : "memory");
 }
 
 // 3D and 4D tiled loads whose completion counts on an mbarrier of either CTA
@@ -272,26 +264,33 @@ __host__ __device__ inline PairUnits pair_units(int pair, int pairs, int64_t uni
 }
 
 // --------------------------------------------------------------- dx = dz W_r
-// Units (256-column strip, 256-token tile), strip-major; a pair takes a run of
-// them.  The strip's W_r (Np experts x 256 columns, half in each CTA) stays in
-// shared memory for the run's tiles; the next strip's 64-expert blocks arrive
-// as the last tile's last pass over each of them ends.  The output goes out
-// through shared memory and TMA stores (or TMA adds, one per element): stores
-// of a TMEM row per thread, 32 bytes to each of 32 rows an instruction, kept
-// the L1 at 78% and took 12 us longer at T = 4096.
-constexpr int X_STAGES = 8;
-constexpr int X_A = 128 * 128;      // 128 tokens x 64 experts
-constexpr int X_BG = 64 * 128;      // 64 experts x 64 columns
-constexpr int X_KB = 4;             // 64-expert blocks at most
-constexpr int X_B = X_KB * 2 * X_BG;  // Np <= 256 experts x 128 columns
-constexpr int X_BOX = 128 * 128;    // 128 tokens x 32 FP32 columns
-constexpr int X_SMEM = 1024 + X_B + X_STAGES * X_A + 2 * X_BOX + 512;
+// Units (256-token tile, 256-column strip), tile-major; a pair takes a run of
+// them.  The parts are three times the bytes of W_r's strip, so they are what
+// stays: a token tile's parts (Np experts x 128 tokens x 3 in each CTA, 192 KB)
+// stay in shared memory over its strips while W_r streams past in stages of 32
+// experts (half a strip's columns in each CTA), 64 KB a unit against 192 KB
+// the other way round (T = 4096, N_r = 256, H = 7168: 43 us that way, 39 us this,
+// where the products alone take 28 us at the library's matrix rate).  The next tile's parts arrive as the current one's last pass over
+// each 64-expert block ends.  The epilogue turns TMEM's
+// rows so that four lanes store 128 contiguous bytes of a row (a row per thread
+// took 64 cycles an instruction in the L1).
+constexpr int X_STAGES = 4;
+constexpr int X_THREADS = 320;        // warp 0 TMA, warp 1 MMA (even CTA), warps 2..9 epilogue
+constexpr int X_AB = 128 * 128;       // 128 tokens x 64 experts, one part
+constexpr int X_KB = 4;               // 64-expert blocks at most
+constexpr int X_A = X_KB * kParts * X_AB;
+constexpr int X_K = 32;               // experts per stage of W_r
+constexpr int X_KPB = 64 / X_K;       // stages per 64-expert block
+constexpr int X_BG = X_K * 128;       // 32 experts x 64 columns
+constexpr int X_B = 2 * X_BG;         // this CTA's 128 columns
+constexpr int X_SMEM = 1024 + X_A + X_STAGES * X_B + 256;
 static_assert(X_SMEM <= 232448, "shared memory budget");
 
 struct DxArgs {
   int64_t T;
   int n_strips, m_tiles, cols;  // H / 256 and T / 256, rounded up; H
   int kb;                       // Np / 64
+  float *dx;
   int accumulate;
   int32_t *err;
   uint64_t limit_ns;
@@ -300,31 +299,69 @@ struct DxArgs {
 struct DxBars {
   uint64_t full[X_STAGES];   // even CTA: the stage of both CTAs has landed
   uint64_t empty[X_STAGES];  // each CTA: the MMAs have read the stage
-  uint64_t bfull[X_KB], bempty[X_KB];
+  uint64_t afull[X_KB], aempty[X_KB];
   uint64_t tfull[2], tempty[2];
   uint64_t teardown;
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(DxBars) <= 512, "barrier block");
+static_assert(sizeof(DxBars) <= 256, "barrier block");
 
-// One 32-column box of 128 rows: this thread's row r, as the tensor map's
-// 128-byte swizzle expects it.
-__device__ __forceinline__ void put_box_row(uint8_t *box, int r, const uint32_t (&v)[32]) {
+// 16 TMEM lanes x 32 columns: r[4 j + 2 i + k] of lane l is row l / 4 + 8 i,
+// column 8 j + 2 (l mod 4) + k.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four lanes hold columns 2 j, 2 j + 1 (j the lane in its four) of blocks
+// 0..3, block b in f[2 b], f[2 b + 1]; afterwards lane j holds the eight columns
+// of block j in order.  Two exchanges, with the lane two and one away.
+__device__ __forceinline__ void quad_transpose(float (&f)[8], int lane) {
+  const bool up2 = lane & 2, up1 = lane & 1;
+  // blocks (0, 1) <-> (2, 3): keep the half of the lane's own pair
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4 *>(box + r * 128 + ((j ^ (r & 7)) << 4)) =
-        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  for (int i = 0; i < 4; ++i) {
+    const float got = __shfl_xor_sync(0xffffffffu, up2 ? f[i] : f[4 + i], 2);
+    if (up2)
+      f[i] = got;
+    else
+      f[4 + i] = got;
+  }
+  // now f[0..3] are the pair's blocks from lanes 0/1 of the four, f[4..7] from lanes 2/3
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float got = __shfl_xor_sync(0xffffffffu, up1 ? f[4 * g + k] : f[4 * g + 2 + k], 1);
+      if (up1)
+        f[4 * g + k] = got;
+      else
+        f[4 * g + 2 + k] = got;
+    }
+  }
+}
+
+// dx += v, one FP32 addition per element
+__device__ __forceinline__ void red_add_v4(float *p, const float4 &v) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
 }
 }  // namespace
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                     const __grid_constant__ CUtensorMap map_o, const DxArgs args) {
+                     const DxArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sb = smem, *sa = sb + X_B, *so = sa + X_STAGES * X_A;
-  DxBars *bars = reinterpret_cast<DxBars *>(so + 2 * X_BOX);
+  uint8_t *sa = smem, *sb = sa + X_A;
+  DxBars *bars = reinterpret_cast<DxBars *>(sb + X_STAGES * X_B);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
@@ -333,8 +370,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
       mbar_init(&bars->empty[i], 1);
     }
     for (int i = 0; i < X_KB; ++i) {
-      mbar_init(&bars->bfull[i], 2);
-      mbar_init(&bars->bempty[i], 1);
+      mbar_init(&bars->afull[i], 2);
+      mbar_init(&bars->aempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
@@ -345,7 +382,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
     fence_mbar_init();
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_w);
-    tma_prefetch_map(&map_o);
   }
   if (warp == 1) {
     tmem_alloc_pair(&bars->tmem_base, 512);
@@ -358,42 +394,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
   const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, static_cast<int64_t>(args.n_strips) * args.m_tiles);
-  const int kb = args.kb, nk = kParts * kb;
+  const int nk = args.kb * X_KPB;  // stages per unit
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint64_t pol = policy_evict_last();  // every strip reads the parts again
-      uint32_t it = 0, nb = 0;  // stages; strips
-      int64_t strip = -1;
+      const uint64_t pol = policy_evict_last();  // every tile reads W_r again
+      uint32_t it = 0, na = 0;  // stages; token tiles
+      int64_t tile = -1;
       bool stop = false;
       for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u) {
         if (*abortp) break;
-        const int m = static_cast<int>(u % args.m_tiles);
-        const bool fresh = u / args.m_tiles != strip;
-        strip = u / args.m_tiles;
-        for (int k = 0; k < nk && !stop; ++k, ++it) {
-          const int s = it % X_STAGES;
-          if (fresh && k < kb) {  // the strip's block of W_r that this step is the first to read
-            if (!mbar_wait(&bars->bempty[k], (nb & 1) ^ 1, ctl)) {
+        const bool fresh = u / args.n_strips != tile;
+        tile = u / args.n_strips;
+        const int strip = static_cast<int>(u % args.n_strips);
+        for (int k = 0; k < nk; ++k, ++it) {
+          if (fresh && k % X_KPB == 0) {  // the first stage that reads this block of the tile's parts
+            const int kb = k / X_KPB;
+            if (!mbar_wait(&bars->aempty[kb], (na & 1) ^ 1, ctl)) {
               stop = true;
               break;
             }
-            const uint32_t bar = mapa_shared(smem_u32(&bars->bfull[k]), 0);
-            mbar_arrive_expect_tx_cluster(bar, 2 * X_BG);
-            for (int g = 0; g < 2; ++g)
-              tma_load_2d_pair(sb + (k * 2 + g) * X_BG, &map_w, bar,
-                               static_cast<int>(strip) * 256 + rank * 128 + g * 64, k * 64, pol);
+            const uint32_t bar = mapa_shared(smem_u32(&bars->afull[kb]), 0);
+            mbar_arrive_expect_tx_cluster(bar, kParts * X_AB);
+            tma_load_4d_pair(sa + kb * kParts * X_AB, &map_a, bar, 0, static_cast<int>(tile) * 256 + rank * 128, kb, 0,
+                             pol);
           }
+          const int s = it % X_STAGES;
           if (!mbar_wait(&bars->empty[s], ((it / X_STAGES) & 1) ^ 1, ctl)) {
             stop = true;
             break;
           }
           const uint32_t bar = mapa_shared(smem_u32(&bars->full[s]), 0);
-          mbar_arrive_expect_tx_cluster(bar, X_A);
-          tma_load_2d_pair(sa + s * X_A, &map_a, bar, (k % kb) * 64,
-                           static_cast<int>((k / kb) * args.T + static_cast<int64_t>(m) * 256 + rank * 128), pol);
+          mbar_arrive_expect_tx_cluster(bar, X_B);
+          tma_load_3d_pair(sb + s * X_B, &map_w, bar, 0, k * X_K, strip * 4 + rank * 2, pol);
         }
-        if (fresh) ++nb;
+        if (fresh) ++na;
       }
       // the stages in flight are read before this CTA may exit
       int quiet = 0;
@@ -403,74 +438,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      uint32_t it = 0, tc = 0, nb = 0;
-      int64_t strip = -1;
+      uint32_t it = 0, tc = 0, na = 0;
+      int64_t tile = -1;
       bool stop = false;
       const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescBMn;
       for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u, ++tc) {
         if (*abortp) break;
-        const bool fresh = u / args.m_tiles != strip;
-        strip = u / args.m_tiles;
-        const bool last = u + 1 < pu.u1 && (u + 1) / args.m_tiles != strip;  // another strip follows
+        const bool fresh = u / args.n_strips != tile;
+        tile = u / args.n_strips;
+        const bool last = u + 1 < pu.u1 && (u + 1) / args.n_strips != tile;  // another token tile follows
         const uint32_t buf = tc & 1;
         if (!mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) break;
         const uint32_t d = tmem + buf * 256;
         for (int k = 0; k < nk; ++k, ++it) {
-          const int s = it % X_STAGES;
-          if ((fresh && k < kb && !mbar_wait(&bars->bfull[k], nb & 1, ctl)) ||
+          const int s = it % X_STAGES, kb = k / X_KPB;
+          if ((fresh && k % X_KPB == 0 && !mbar_wait(&bars->afull[kb], na & 1, ctl)) ||
               !mbar_wait(&bars->full[s], (it / X_STAGES) & 1, ctl)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint64_t da = sw128_kmajor_desc(smem_u32(sa + s * X_A));
-          const uint64_t db = sw128_mnmajor_desc(smem_u32(sb + (k % kb) * 2 * X_BG), X_BG);
+          const uint64_t da = sw128_kmajor_desc(smem_u32(sa + kb * kParts * X_AB)) + (k % X_KPB) * (X_K * 2 >> 4);
+          const uint64_t db = sw128_mnmajor_desc(smem_u32(sb + s * X_B), X_BG);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            umma_bf16_pair(d, da + 2 * q, db + (2048 >> 4) * q, idesc, (k > 0 || q > 0) ? 1u : 0u);
+          for (int q = 0; q < X_K / 16; ++q)
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+              umma_bf16_pair(d, da + p * (X_AB >> 4) + 2 * q, db + (2048 >> 4) * q, idesc,
+                             (k > 0 || q > 0 || p > 0) ? 1u : 0u);
           umma_commit_pair(&bars->empty[s], 0x3);
-          if (last && k >= nk - kb) umma_commit_pair(&bars->bempty[k % kb], 0x3);
+          if (last && k % X_KPB == X_KPB - 1) umma_commit_pair(&bars->aempty[kb], 0x3);
         }
         umma_commit_pair(&bars->tfull[buf], 0x3);
-        if (fresh) ++nb;
+        if (fresh) ++na;
       }
       int quiet = 0;
       const WaitCtl drain{&quiet, nullptr, 100000000ull};
       umma_commit_pair(&bars->teardown, 0x1);
       mbar_wait(&bars->teardown, 0, drain);
     }
-  } else if (warp >= 4) {
-    const int q = warp & 3;          // TMEM lane quarter
-    const int wg = (warp - 4) >> 2;  // column half: its four warps share a box and named barrier 1 + wg
-    const int r = q * 32 + lane;
-    const bool issuer = q == 0 && lane == 0;
-    uint8_t *box = so + wg * X_BOX;
+  } else {
+    const int q = warp & 3;           // TMEM lane quarter
+    const int half = (warp - 2) >> 2;  // column half
+    const bool wide = (reinterpret_cast<uintptr_t>(args.dx) & 31) == 0;
     uint32_t tc = 0;
     for (int64_t u = pu.u0; u < pu.u1; ++u, ++tc) {
       const uint32_t buf = tc & 1;
-      const bool ok = mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl);
-      if (named_bar_or(1 + wg, 128, !ok)) break;  // the four warps leave together
+      if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) break;
       tc_fence_after();
-      const int y = static_cast<int>(u % args.m_tiles) * 256 + rank * 128;
-      const int x0 = static_cast<int>(u / args.m_tiles) * 256 + wg * 128;
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
-      if (x0 < args.cols && y < args.T) {  // H is a multiple of 128: a column half is in or out
+      const int64_t t0 = (u / args.n_strips) * 256 + rank * 128 + q * 32;
+      const int x0 = static_cast<int>(u % args.n_strips) * 256 + half * 128;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * 128;
+      // H is a multiple of 128: a column half is in or out
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(ta + c * 32, v);
+      for (int c = 0; c < 4 && x0 < args.cols; ++c) {
+        // 16 rows at a time: lane 4 i + j gets rows i and i + 8, columns 2 j and
+        // 2 j + 1 of each of the four 8-column blocks; turned within each four
+        // lanes so that lane j has block j whole, 32 bytes
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[16];
+          tmem_ld_16x256(ta + c * 32 + (h << 20), v);
           tmem_ld_wait();
-          if (issuer) bulk_wait_read();  // the box's last store has read it
-          named_bar_sync(1 + wg, 128);
-          put_box_row(box, r, v);
-          fence_proxy_async_smem();
-          named_bar_sync(1 + wg, 128);
-          if (issuer) {
-            if (args.accumulate)
-              tma_reduce_add_2d(&map_o, box, x0 + c * 32, y);
-            else
-              tma_store_2d(&map_o, box, x0 + c * 32, y);
-            bulk_commit();
+#pragma unroll
+          for (int r8 = 0; r8 < 2; ++r8) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = __uint_as_float(v[4 * j + 2 * r8]);
+              f[2 * j + 1] = __uint_as_float(v[4 * j + 2 * r8 + 1]);
+            }
+            quad_transpose(f, lane);
+            const int64_t t = t0 + h * 16 + r8 * 8 + (lane >> 2);
+            if (t < args.T) {
+              float *dst = args.dx + t * args.cols + x0 + c * 32 + (lane & 3) * 8;
+              if (args.accumulate) {
+                red_add_v4(dst, make_float4(f[0], f[1], f[2], f[3]));
+                red_add_v4(dst + 4, make_float4(f[4], f[5], f[6], f[7]));
+              } else if (wide) {
+                st_f32x8(dst, f);
+              } else {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+              }
+            }
           }
         }
       }
@@ -478,7 +529,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
     }
-    if (issuer) bulk_wait_all();
   }
   // neither CTA leaves (or frees TMEM) while the other still works with its
   // shared memory, barriers or TMEM
@@ -500,6 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
 // A stage is two loads, one 4D box of the parts and one 3D box of x: as eight
 // 2D boxes of 32 tokens each load cost about 110 ns and set the pace.
 namespace {
+constexpr int WR_THREADS = 384;              // warp 0 TMA, warp 1 MMA (even CTA), warps 4..11 epilogue
 constexpr int WR_STAGES = 3;
 constexpr int WR_TOK = 64;                   // tokens (K) per stage
 constexpr int WR_CHUNK = 4;                  // stages per TMEM accumulation
@@ -537,7 +588,7 @@ struct DwrBars {
 static_assert(sizeof(DwrBars) <= 256, "barrier block");
 }  // namespace
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RP_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
     router_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                       const DwrArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -772,21 +823,22 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
 cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
                              int32_t *err, uint64_t limit_ns, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
-  const int Np = router_parts_pitch(Nr);
-  CUtensorMap ma, mw, mo;
-  if (moe_host::encode_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, Np, kParts * T,
-                               static_cast<uint64_t>(Np) * 2, 64, 128) != 0 ||
-      moe_host::encode_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wr, H, Nr, static_cast<uint64_t>(H) * 2, 64,
-                               64) != 0 ||
-      moe_host::encode_tmap_2d(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx, H, T, static_cast<uint64_t>(H) * 4, 32,
-                               128) != 0)
+  const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
+  // in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], W_r [H / 64][Nr][64]
+  const uint64_t da[4] = {64, t, Np / 64, kParts}, sa[3] = {Np * 2, 128, t * Np * 2};
+  const uint64_t dw[3] = {64, static_cast<uint64_t>(Nr), h / 64}, sw[2] = {h * 2, 128};
+  const uint32_t ba[4] = {64, 128, 1, kParts}, bw[3] = {64, X_K, 2};
+  CUtensorMap ma, mw;
+  if (moe_host::encode_tmap(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, 4, da, sa, ba) != 0 ||
+      moe_host::encode_tmap(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wr, 3, dw, sw, bw) != 0)
     return cudaErrorInvalidValue;
   DxArgs a{};
   a.T = T;
   a.cols = H;
   a.n_strips = strips_of(H);
   a.m_tiles = static_cast<int>((T + 255) / 256);
-  a.kb = Np / 64;
+  a.kb = static_cast<int>(Np / 64);
+  a.dx = dx;
   a.accumulate = accumulate;
   a.err = err;
   a.limit_ns = limit_ns;
@@ -794,10 +846,10 @@ cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int N
   if (const cudaError_t e = smem_attr_once(router_dx_kernel, X_SMEM, attr_done)) return e;
   const int64_t units = static_cast<int64_t>(a.n_strips) * a.m_tiles;
   static std::atomic<int> resident[64];
-  int64_t pairs = resident_pairs(router_dx_kernel, RP_THREADS, X_SMEM, most_pairs(), resident);
+  int64_t pairs = resident_pairs(router_dx_kernel, X_THREADS, X_SMEM, most_pairs(), resident);
   if (pairs > units) pairs = units;
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  router_dx_kernel<<<static_cast<unsigned>(2 * pairs), RP_THREADS, X_SMEM, st>>>(ma, mw, mo, a);
+  router_dx_kernel<<<static_cast<unsigned>(2 * pairs), X_THREADS, X_SMEM, st>>>(ma, mw, a);
   return cudaGetLastError();
 }
 
@@ -824,10 +876,10 @@ cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int N
   static std::atomic<uint64_t> attr_done{0};
   if (const cudaError_t e = smem_attr_once(router_dwr_kernel, WR_SMEM, attr_done)) return e;
   static std::atomic<int> resident[64];
-  int64_t pairs = resident_pairs(router_dwr_kernel, RP_THREADS, WR_SMEM, most_pairs(), resident);
+  int64_t pairs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident);
   if (pairs > dwr_pairs(T, H)) pairs = dwr_pairs(T, H);
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  router_dwr_kernel<<<static_cast<unsigned>(2 * pairs), RP_THREADS, WR_SMEM, st>>>(ma, mx, a);
+  router_dwr_kernel<<<static_cast<unsigned>(2 * pairs), WR_THREADS, WR_SMEM, st>>>(ma, mx, a);
   if (const cudaError_t e = cudaGetLastError()) return e;
   const int64_t n4 = static_cast<int64_t>(Nr) * H / 4;
   dwr_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, st>>>(part, static_cast<int>(pairs), a.n_strips,
