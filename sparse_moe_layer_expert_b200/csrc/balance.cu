@@ -13,6 +13,7 @@
 // does not depend on the schedule.
 #include "common.cuh"
 #include "kernels.h"
+#include "operators.cuh"
 #include "router_math.cuh"
 
 namespace moe {
@@ -36,13 +37,14 @@ struct BalArgs {
 };
 }  // namespace
 
-template <bool VEC>
-__global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const BalArgs a) {
+template <bool VEC, int B>
+__global__ void __launch_bounds__(BAL_WARPS * 32, B == 1 ? 4 : 2) balance_pieces_kernel(const BalArgs a) {
   __shared__ __align__(16) float p_sh[BAL_WARPS][EPL * 32];
   __shared__ int c_sh[EPL * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t c1 = c0 + a.chunk < a.T ? c0 + a.chunk : a.T;
+  dependents_start();
   bool bad = false;
   int64_t t0 = c0;
   while (t0 < c1) {  // every turn moves t0 forward, whatever the offsets hold
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const Ba
       int e = 0;
       if (lane < a.Kr) e = a.idx[t * a.Kr + lane];
       float v[EPL];
-      load_logits<VEC>(a.partial, a.n_ks, a.T, a.Nr, t, lane, v);
+      load_logits<VEC, B>(a.partial, a.n_ks, a.T, a.Nr, t, lane, v);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
@@ -104,39 +106,58 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) balance_pieces_kernel(const Ba
   if (bad) atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
 }
 
-// One CTA per sequence: four slices of 256 threads take every fourth piece.
-__global__ void __launch_bounds__(1024) balance_join_kernel(const BalArgs a, float alpha, float *__restrict__ loss,
-                                                             int32_t *__restrict__ counts) {
-  __shared__ float p_sh[4][256];
-  __shared__ int c_sh[4][256];
+// One CTA per sequence: 16 slices of 64 threads, 4 experts a thread, each
+// slice taking every 16th piece; then the slices in order.
+constexpr int BAL_SLICES = 16;
+
+__global__ void __launch_bounds__(BAL_SLICES * 64) balance_join_kernel(const BalArgs a, float alpha,
+                                                                       float *__restrict__ loss,
+                                                                       int32_t *__restrict__ counts) {
+  __shared__ float p_sh[BAL_SLICES][256];
+  __shared__ int c_sh[BAL_SLICES][256];
   __shared__ float term[8];
   const int s = blockIdx.x;
-  const int e = threadIdx.x & 255, sl = threadIdx.x >> 8;
+  const int e0 = (threadIdx.x & 63) * 4, sl = threadIdx.x >> 6;
   int64_t b0 = a.off[s], b1 = a.off[s + 1];
   if (b0 < 0 || b1 < b0 || b1 > a.T) {  // wrong offsets: reported, and read as an empty sequence
     if (threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
     b0 = b1 = 0;
   }
-  float p = 0.0f;
-  int c = 0;
-  if (e < a.Nr && b1 > b0) {
-    const int64_t k0 = b0 / a.chunk, k1 = (b1 - 1) / a.chunk;
-    for (int64_t k = k0 + sl; k <= k1; k += 4) {
-      p += a.p_part[(k + s) * a.Nr + e];
-      c += a.c_part[(k + s) * a.Nr + e];
+  float p[4] = {0.f, 0.f, 0.f, 0.f};
+  int c[4] = {0, 0, 0, 0};
+  predecessor_done();
+  if (e0 < a.Nr && b1 > b0) {
+    const int k0 = static_cast<int>(b0 / a.chunk), k1 = static_cast<int>((b1 - 1) / a.chunk);
+    const int n = a.Nr - e0 < 4 ? a.Nr - e0 : 4;
+#pragma unroll 4
+    for (int k = k0 + sl; k <= k1; k += BAL_SLICES) {
+      const int64_t at = static_cast<int64_t>(k + s) * a.Nr + e0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) {
+          p[j] += a.p_part[at + j];
+          c[j] += a.c_part[at + j];
+        }
     }
   }
-  p_sh[sl][e] = p;
-  c_sh[sl][e] = c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    p_sh[sl][e0 + j] = p[j];
+    c_sh[sl][e0 + j] = c[j];
+  }
   __syncthreads();
   if (threadIdx.x < 256) {
-    p = (p_sh[0][e] + p_sh[1][e]) + (p_sh[2][e] + p_sh[3][e]);
-    c = c_sh[0][e] + c_sh[1][e] + c_sh[2][e] + c_sh[3][e];
-    if (e < a.Nr) counts[static_cast<int64_t>(s) * a.Nr + e] = c;
-    float v = e < a.Nr ? static_cast<float>(c) * p : 0.0f;
+    const int e = threadIdx.x;
+    float ps = 0.0f;
+    int cs = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) term[threadIdx.x >> 5] = v;
+    for (int i = 0; i < BAL_SLICES; ++i) {
+      ps += p_sh[i][e];
+      cs += c_sh[i][e];
+    }
+    if (e < a.Nr) counts[static_cast<int64_t>(s) * a.Nr + e] = cs;
+    const float v = warp_sum(e < a.Nr ? static_cast<float>(cs) * ps : 0.0f);
+    if ((e & 31) == 0) term[e >> 5] = v;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -180,14 +201,12 @@ cudaError_t launch_balance_loss(const float *partial, int n_ks, int64_t T, int N
   a.c_part = c_part;
   a.err = err;
   if (T > 0) {
-    if (Nr % 4 == 0)
-      balance_pieces_kernel<true><<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
-    else
-      balance_pieces_kernel<false><<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
+    auto kernel = Nr % 4 == 0 ? (n_ks < 4 ? balance_pieces_kernel<true, 1> : balance_pieces_kernel<true, 4>)
+                              : (n_ks < 4 ? balance_pieces_kernel<false, 1> : balance_pieces_kernel<false, 4>);
+    kernel<<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
   }
   if (const cudaError_t e = cudaGetLastError()) return e;
-  balance_join_kernel<<<n_seq, 1024, 0, st>>>(a, alpha, loss, counts);
-  return cudaGetLastError();
+  return launch_next(balance_join_kernel, dim3(n_seq), dim3(BAL_SLICES * 64), 0, st, a, alpha, loss, counts);
 }
 
 }  // namespace moe

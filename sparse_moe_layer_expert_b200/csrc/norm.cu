@@ -218,6 +218,7 @@ struct NormBwd {
 template <typename TY, typename TS, typename TX, int CH>
 __global__ void __launch_bounds__(1024, 1) add_rmsnorm_bwd_kernel(const NormBwd p) {
   __shared__ float buf[2][32];
+  dependents_start();
   const int nch = p.cols / 8;
   float dw[CH][8];
 #pragma unroll
@@ -411,6 +412,7 @@ template <typename TY, typename TS, typename TX, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int stages) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) RingBars bars;
+  dependents_start();
   const int nch = p.cols / 8;
   const uint32_t y_bytes = static_cast<uint32_t>(p.cols * sizeof(TY)), s_bytes = static_cast<uint32_t>(p.cols * sizeof(TS));
   const uint32_t stage_bytes = y_bytes + (p.dres ? 2 * s_bytes : s_bytes);
@@ -498,6 +500,8 @@ __global__ void __launch_bounds__(1024) norm_dw_join_kernel(const float *__restr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
+  predecessor_done();
+#pragma unroll 4
   for (int i = warp; i < n_part; i += 32) s += part[static_cast<int64_t>(i) * cols + c];
   sh[warp][lane] = s;
   __syncthreads();
@@ -655,8 +659,8 @@ cudaError_t launch_add_rmsnorm_bwd(const void *dy, bool dy_f32, const void *h, c
     e = f32 ? (dx_f32 ? launch_norm_bwd<B, float, float>(p, &n, st) : launch_norm_bwd<B, float, B>(p, &n, st))
             : (dx_f32 ? launch_norm_bwd<B, B, float>(p, &n, st) : launch_norm_bwd<B, B, B>(p, &n, st));
   if (e != cudaSuccess || !dw) return e;
-  norm_dw_join_kernel<<<cols / 32, 1024, 0, st>>>(part, n, cols, dw);
-  return cudaGetLastError();
+  return launch_next(norm_dw_join_kernel, dim3(static_cast<unsigned>(cols / 32)), dim3(1024), 0, st,
+                     static_cast<const float *>(part), n, cols, dw);
 }
 
 }  // namespace moe

@@ -2,9 +2,35 @@
 // router_bwd.cu) beside those of common.cuh.
 #pragma once
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace moe {
+
+// Kernels of one call that follow each other on a stream start early
+// (programmatic dependent launch): a kernel lets its successor begin while it
+// still runs (dependents_start), and a kernel launched by launch_next waits,
+// behind its own set-up, until its predecessor is complete and its writes are
+// visible (predecessor_done: before any access to memory that another kernel
+// writes or reads).  Worth about 2 us an edge.
+__device__ __forceinline__ void dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void predecessor_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // Eight consecutive floats, one 32-byte sector (p 32-byte aligned).
 __device__ __forceinline__ void st_f32x8(float *p, const float *v) {

@@ -87,11 +87,12 @@ __device__ __forceinline__ void split3(float v, uint32_t (&o)[3]) {
 
 // A warp takes `run` consecutive tokens; the load factors f of the sequence it
 // is in stay in registers from token to token.
-template <bool VEC>
-__global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
+template <bool VEC, int B>
+__global__ void __launch_bounds__(256, B == 1 ? 4 : 2) router_dz_kernel(const DzArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t t0 = w * a.run, t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
+  dependents_start();
   int seq = -1;           // sequence whose f is held
   int64_t seq_end = t0;   // look for a sequence at the first token
   float f[EPL], kk = 0.0f;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
     }
     if (a.off) {
       float z[EPL];
-      load_logits<VEC>(a.partial, a.n_ks, a.T, a.Nr, t, lane, z);
+      load_logits<VEC, B>(a.partial, a.n_ks, a.T, a.Nr, t, lane, z);
       if (t >= seq_end) {
         const int s = seq_of(a.off, a.n_seq, t);
         seq = -1;
@@ -159,9 +160,7 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
           atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
           e = -1;
         } else {
-          float z = 0.0f;
-          for (int k = 0; k < a.n_ks; ++k) z += __ldg(a.partial + (static_cast<int64_t>(k) * a.T + t) * a.Nr + e);
-          sigmoid_pair(z, s, om);
+          sigmoid_pair(load_logit<B>(a.partial, a.n_ks, a.T, a.Nr, t, e), s, om);
         }
       }
       const float sum = warp_sum(s);
@@ -256,11 +255,14 @@ __device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *m
       : "memory");
 }
 
-struct PairUnits {  // this pair's units [u0, u1) of n * per, in order
-  int64_t u0, u1;
+// A pair's run [u0, u1) of the launch's units, in order.  (At most 2^14 stages
+// of 2^20 tokens times 128 strips of 32768 columns, times the pairs: 2^28.)
+struct PairUnits {
+  int u0, u1;
 };
-__host__ __device__ inline PairUnits pair_units(int pair, int pairs, int64_t units) {
-  return PairUnits{pair * units / pairs, (pair + 1) * units / pairs};
+__host__ __device__ inline PairUnits pair_units(int pair, int pairs, int units) {
+  return PairUnits{static_cast<int>(static_cast<uint32_t>(pair) * units / pairs),
+                   static_cast<int>(static_cast<uint32_t>(pair + 1) * units / pairs)};
 }
 
 // --------------------------------------------------------------- dx = dz W_r
@@ -393,20 +395,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   const uint32_t tmem = bars->tmem_base;
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
-  const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, static_cast<int64_t>(args.n_strips) * args.m_tiles);
+  const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, args.n_strips * args.m_tiles);
   const int nk = args.kb * X_KPB;  // stages per unit
+  dependents_start();
+  predecessor_done();
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_last();  // every tile reads W_r again
       uint32_t it = 0, na = 0;  // stages; token tiles
-      int64_t tile = -1;
+      int tile = -1;
       bool stop = false;
-      for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u) {
+      for (int u = pu.u0; u < pu.u1 && !stop; ++u) {
         if (*abortp) break;
         const bool fresh = u / args.n_strips != tile;
         tile = u / args.n_strips;
-        const int strip = static_cast<int>(u % args.n_strips);
+        const int strip = u % args.n_strips;
         for (int k = 0; k < nk; ++k, ++it) {
           if (fresh && k % X_KPB == 0) {  // the first stage that reads this block of the tile's parts
             const int kb = k / X_KPB;
@@ -416,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
             }
             const uint32_t bar = mapa_shared(smem_u32(&bars->afull[kb]), 0);
             mbar_arrive_expect_tx_cluster(bar, kParts * X_AB);
-            tma_load_4d_pair(sa + kb * kParts * X_AB, &map_a, bar, 0, static_cast<int>(tile) * 256 + rank * 128, kb, 0,
+            tma_load_4d_pair(sa + kb * kParts * X_AB, &map_a, bar, 0, tile * 256 + rank * 128, kb, 0,
                              pol);
           }
           const int s = it % X_STAGES;
@@ -439,10 +443,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       uint32_t it = 0, tc = 0, na = 0;
-      int64_t tile = -1;
+      int tile = -1;
       bool stop = false;
       const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescBMn;
-      for (int64_t u = pu.u0; u < pu.u1 && !stop; ++u, ++tc) {
+      for (int u = pu.u0; u < pu.u1 && !stop; ++u, ++tc) {
         if (*abortp) break;
         const bool fresh = u / args.n_strips != tile;
         tile = u / args.n_strips;
@@ -482,12 +486,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
     const int half = (warp - 2) >> 2;  // column half
     const bool wide = (reinterpret_cast<uintptr_t>(args.dx) & 31) == 0;
     uint32_t tc = 0;
-    for (int64_t u = pu.u0; u < pu.u1; ++u, ++tc) {
+    for (int u = pu.u0; u < pu.u1; ++u, ++tc) {
       const uint32_t buf = tc & 1;
       if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) break;
       tc_fence_after();
-      const int64_t t0 = (u / args.n_strips) * 256 + rank * 128 + q * 32;
-      const int x0 = static_cast<int>(u % args.n_strips) * 256 + half * 128;
+      const int64_t t0 = static_cast<int64_t>(u / args.n_strips) * 256 + rank * 128 + q * 32;
+      const int x0 = (u % args.n_strips) * 256 + half * 128;
       const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * 128;
       // H is a multiple of 128: a column half is in or out
 #pragma unroll 1
@@ -563,8 +567,8 @@ static_assert(WR_SMEM <= 232448, "shared memory budget");
 
 // A pair's run [u, end) of one strip, and how its stages fall into chunks: the
 // MMA issuer and the epilogue walk it alike.
-__device__ __forceinline__ int64_t run_end(int64_t u, int64_t u1, int64_t per_strip) {
-  const int64_t e = (u / per_strip + 1) * per_strip;
+__device__ __forceinline__ int run_end(int u, int u1, int per_strip) {
+  const int e = (u / per_strip + 1) * per_strip;
   return e < u1 ? e : u1;
 }
 
@@ -622,7 +626,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
   const int pair = blockIdx.x >> 1;
-  const PairUnits pu = pair_units(pair, gridDim.x >> 1, static_cast<int64_t>(args.n_strips) * args.n_stages);
+  const PairUnits pu = pair_units(pair, gridDim.x >> 1, args.n_strips * args.n_stages);
+
+  dependents_start();
+  predecessor_done();
 
   // Register split as in gemm_pair.cu: 128 * 72 + 256 * 216 = 384 * 168
   if (warp < 4) {
@@ -632,14 +639,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
         const uint64_t pol_a = policy_evict_last();   // every strip reads the parts again
         const uint64_t pol_x = policy_evict_first();  // x is read once
         uint32_t it = 0;
-        for (int64_t u = pu.u0; u < pu.u1; ++u, ++it) {
+        for (int u = pu.u0; u < pu.u1; ++u, ++it) {
           const int s = it % WR_STAGES;
           if (*abortp || !mbar_wait(&bars->empty[s], ((it / WR_STAGES) & 1) ^ 1, ctl)) break;
           uint8_t *st = smem + s * WR_STAGE;
           const uint32_t bar = mapa_shared(smem_u32(&bars->full[s]), 0);
-          const int t0 = static_cast<int>(u % args.n_stages) * WR_TOK;
+          const int t0 = (u % args.n_stages) * WR_TOK;
           mbar_arrive_expect_tx_cluster(bar, WR_STAGE);
-          tma_load_3d_pair(st + WR_A, &map_x, bar, 0, t0, static_cast<int>(u / args.n_stages) * 4 + rank * 2, pol_x);
+          tma_load_3d_pair(st + WR_A, &map_x, bar, 0, t0, (u / args.n_stages) * 4 + rank * 2, pol_x);
           tma_load_4d_pair(st, &map_a, bar, 0, t0, rank * 2, 0, pol_a);
         }
         int quiet = 0;
@@ -653,8 +660,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
         uint32_t it = 0, tc = 0;
         bool stop = false;
         const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescAMn | kIdescBMn;
-        for (int64_t u = pu.u0; u < pu.u1 && !stop;) {
-          const int64_t end = run_end(u, pu.u1, args.n_stages);
+        for (int u = pu.u0; u < pu.u1 && !stop;) {
+          const int end = run_end(u, pu.u1, args.n_stages);
           for (; u < end && !stop; ++tc) {
             const uint32_t buf = tc & 1;
             if (*abortp || !mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) {
@@ -697,9 +704,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
     const bool live = rank * 128 + q * 32 < args.Nr;     // any expert in this warp
     uint32_t tc = 0;
     bool stop = false;
-    for (int64_t u = pu.u0; u < pu.u1 && !stop;) {
-      const int64_t strip = u / args.n_stages;
-      const int64_t end = run_end(u, pu.u1, args.n_stages);
+    for (int u = pu.u0; u < pu.u1 && !stop;) {
+      const int strip = u / args.n_stages;
+      const int end = run_end(u, pu.u1, args.n_stages);
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
@@ -726,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
       }
       if (row < args.Nr) {
-        float *o = args.part + ((pair + strip) * 256 + row) * 256 + wg * 128;
+        float *o = args.part + (static_cast<int64_t>(pair + strip) * 256 + row) * 256 + wg * 128;
 #pragma unroll
         for (int j = 0; j < 128; j += 8) st_f32x8(o + j, acc + j);
       }
@@ -739,28 +746,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// dW_r [Nr, cols] from the pieces of each strip, in token order; 4 columns a
-// thread.
+// dW_r [Nr, cols] from the pieces of each strip, in token order.  CTA (4
+// experts, strip): 64 threads of 4 columns for each expert.  A strip has
+// pairs / n_strips + 2 pieces at most; four are read at once.
 __global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__ part, int pairs, int n_strips,
                                                         int n_stages, int Nr, int cols, float *__restrict__ out) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4;
-  if (i >= static_cast<int64_t>(Nr) * cols) return;
-  const int e = static_cast<int>(i / cols), c = static_cast<int>(i % cols);
-  const int strip = c >> 8;
-  const int64_t units = static_cast<int64_t>(n_strips) * n_stages;
-  const int64_t a = static_cast<int64_t>(strip) * n_stages, b = a + n_stages;  // the strip's units
-  int p = static_cast<int>(a * pairs / units);  // a pair at or before the first one with a share
-  while (pair_units(p, pairs, units).u1 <= a) ++p;
+  const int strip = blockIdx.y;
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+  const int units = n_strips * n_stages;
+  const int a = strip * n_stages, b = a + n_stages;  // the strip's units
+  // the first pair whose run ends behind a, and the first that starts at or behind b
+  int p0 = static_cast<int>(static_cast<uint32_t>(a) * pairs / units), p1 = p0;
+  while (pair_units(p0, pairs, units).u1 <= a) ++p0;
+  p1 = p0;
+  while (p1 < pairs && pair_units(p1, pairs, units).u0 < b) ++p1;
+  predecessor_done();
+  if (e >= Nr || strip * 256 + c >= cols) return;
+  const float *src = part + (static_cast<int64_t>(p0 + strip) * 256 + e) * 256 + c;
+  const int n = p1 - p0;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (; p < pairs && pair_units(p, pairs, units).u0 < b; ++p) {
-    const float4 v = *reinterpret_cast<const float4 *>(part + ((static_cast<int64_t>(p) + strip) * 256 + e) * 256 +
-                                                       (c & 255));
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  for (int i = 0; i < n; i += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < n) v[k] = *reinterpret_cast<const float4 *>(src + (i + k) * 65536ll);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < n) {
+        s.x += v[k].x;
+        s.y += v[k].y;
+        s.z += v[k].z;
+        s.w += v[k].w;
+      }
   }
-  *reinterpret_cast<float4 *>(out + i) = s;
+  *reinterpret_cast<float4 *>(out + static_cast<int64_t>(e) * cols + strip * 256 + c) = s;
 }
 
 // -------------------------------------------------------------------- host
@@ -813,10 +832,9 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
   const int64_t run = (g.T + warps - 1) / warps;
   a.run = static_cast<int>(run < 8 ? run : 8);
   const unsigned grid = static_cast<unsigned>(((g.T + a.run - 1) / a.run + 7) / 8);
-  if (g.Nr % 4 == 0)
-    router_dz_kernel<true><<<grid, 256, 0, st>>>(a);
-  else
-    router_dz_kernel<false><<<grid, 256, 0, st>>>(a);
+  auto kernel = g.Nr % 4 == 0 ? (g.n_ks < 4 ? router_dz_kernel<true, 1> : router_dz_kernel<true, 4>)
+                              : (g.n_ks < 4 ? router_dz_kernel<false, 1> : router_dz_kernel<false, 4>);
+  kernel<<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -844,13 +862,12 @@ cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int N
   a.limit_ns = limit_ns;
   static std::atomic<uint64_t> attr_done{0};
   if (const cudaError_t e = smem_attr_once(router_dx_kernel, X_SMEM, attr_done)) return e;
-  const int64_t units = static_cast<int64_t>(a.n_strips) * a.m_tiles;
+  const int units = a.n_strips * a.m_tiles;
   static std::atomic<int> resident[64];
   int64_t pairs = resident_pairs(router_dx_kernel, X_THREADS, X_SMEM, most_pairs(), resident);
   if (pairs > units) pairs = units;
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  router_dx_kernel<<<static_cast<unsigned>(2 * pairs), X_THREADS, X_SMEM, st>>>(ma, mw, a);
-  return cudaGetLastError();
+  return launch_next(router_dx_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(X_THREADS), X_SMEM, st, ma, mw, a);
 }
 
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
@@ -879,12 +896,12 @@ cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int N
   int64_t pairs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident);
   if (pairs > dwr_pairs(T, H)) pairs = dwr_pairs(T, H);
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  router_dwr_kernel<<<static_cast<unsigned>(2 * pairs), WR_THREADS, WR_SMEM, st>>>(ma, mx, a);
-  if (const cudaError_t e = cudaGetLastError()) return e;
-  const int64_t n4 = static_cast<int64_t>(Nr) * H / 4;
-  dwr_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, st>>>(part, static_cast<int>(pairs), a.n_strips,
-                                                                         a.n_stages, Nr, H, dwr);
-  return cudaGetLastError();
+  cudaError_t e = launch_next(router_dwr_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(WR_THREADS), WR_SMEM, st,
+                              ma, mx, a);
+  if (e != cudaSuccess) return e;
+  return launch_next(dwr_join_kernel, dim3(static_cast<unsigned>((Nr + 3) / 4), static_cast<unsigned>(a.n_strips)),
+                     dim3(256), 0, st, static_cast<const float *>(part), static_cast<int>(pairs), a.n_strips, a.n_stages,
+                     Nr, H, dwr);
 }
 
 }  // namespace moe

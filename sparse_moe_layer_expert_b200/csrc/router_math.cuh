@@ -25,33 +25,78 @@ __device__ __forceinline__ float affinity(const float *__restrict__ partial, int
 __device__ __forceinline__ int lane_expert(int lane, int i) { return (i >> 2) * 128 + lane * 4 + (i & 3); }
 
 // The token's logits: the K splits are added in split order (as affinity()),
-// every split's loads issued together.  VEC: N_r % 4 == 0 (16-byte loads).
-// Experts behind N_r give 0.
-template <bool VEC>
+// B splits' loads under way at once at least.  VEC: N_r % 4 == 0 (16-byte loads).
+// Experts behind N_r give 0.  B = 1 where the router has few splits, as it does
+// for many tokens; with B = 4 a kernel takes twice the registers, which only
+// pays where few tokens (and 4 to 16 splits) leave the SMs' registers free.
+template <bool VEC, int B>
+__device__ __forceinline__ void add_splits(const float *__restrict__ row, int64_t pitch, int Nr, int lane,
+                                           float (&z)[EPL]) {
+  if (VEC) {
+    float4 v[B][2];
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (g * 128 + lane * 4 < Nr)
+          v[k][g] = __ldg(reinterpret_cast<const float4 *>(row + k * pitch + g * 128 + lane * 4));
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (g * 128 + lane * 4 < Nr) {
+          z[4 * g] += v[k][g].x;
+          z[4 * g + 1] += v[k][g].y;
+          z[4 * g + 2] += v[k][g].z;
+          z[4 * g + 3] += v[k][g].w;
+        }
+  } else {
+    float v[B][EPL];
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane_expert(lane, i) < Nr) v[k][i] = __ldg(row + k * pitch + lane_expert(lane, i));
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane_expert(lane, i) < Nr) z[i] += v[k][i];
+  }
+}
+
+template <bool VEC, int B>
 __device__ __forceinline__ void load_logits(const float *__restrict__ partial, int n_ks, int64_t T, int Nr, int64_t t,
                                             int lane, float (&z)[EPL]) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) z[i] = 0.0f;
+  const int64_t pitch = T * Nr;
+  const float *row = partial + t * Nr;
+  int k = 0;
+  if (B > 1)
+    for (; k + B <= n_ks; k += B) add_splits<VEC, B>(row + k * pitch, pitch, Nr, lane, z);
 #pragma unroll 2
-  for (int k = 0; k < n_ks; ++k) {
-    const float *row = partial + (static_cast<int64_t>(k) * T + t) * Nr;
-    if (VEC) {
+  for (; k < n_ks; ++k) add_splits<VEC, 1>(row + k * pitch, pitch, Nr, lane, z);
+}
+
+// One expert's logit, in the same order.
+template <int B>
+__device__ __forceinline__ float load_logit(const float *__restrict__ partial, int n_ks, int64_t T, int Nr, int64_t t,
+                                            int e) {
+  const int64_t pitch = T * Nr;
+  const float *p = partial + t * Nr + e;
+  float z = 0.0f;
+  int k = 0;
+  if (B > 1)
+    for (; k + B <= n_ks; k += B) {
+      float v[B];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g * 128 + lane * 4 < Nr) {
-          const float4 v = __ldg(reinterpret_cast<const float4 *>(row + g * 128 + lane * 4));
-          z[4 * g] += v.x;
-          z[4 * g + 1] += v.y;
-          z[4 * g + 2] += v.z;
-          z[4 * g + 3] += v.w;
-        }
-      }
-    } else {
+      for (int i = 0; i < B; ++i) v[i] = __ldg(p + (k + i) * pitch);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (lane_expert(lane, i) < Nr) z[i] += __ldg(row + lane_expert(lane, i));
+      for (int i = 0; i < B; ++i) z += v[i];
     }
-  }
+  for (; k < n_ks; ++k) z += __ldg(p + k * pitch);
+  return z;
 }
 
 // s and 1 - s.  For z >= 0, 1 - s = e^-z s (1 - s itself would cancel); below,
