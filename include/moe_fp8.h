@@ -325,7 +325,8 @@ MOE_API int moe_profile_events(void *const *events, int32_t n_events);
  *   over expert e's tokens (both operands 128x1 along tokens: one scale per
  *   channel per 128 tokens, a ragged last tile shorter; every GEMM promotes
  *   each 128-long partial into FP32).
- * The gates' own gradient (router backward) is not part of this.
+ * The gates' own gradient is not part of this (moe_router_backward,
+ * moe_block_backward).
  *
  * moe_transpose_weights (set-up): the dgrad GEMMs' weights, each expert's
  * codes and 128x128 block scales transposed:
@@ -611,6 +612,46 @@ MOE_API int moe_router_backward(const moe_config *cfg, const float *logits_dev, 
                                 const moe_balance_grad *balance, const void *x_dev, const void *wr_dev,
                                 float *dlogits_dev, float *dx_dev, int32_t dx_accumulate, float *dwr_dev, void *ws_dev,
                                 size_t ws_bytes, int32_t *err_flag_dev, void *stream);
+
+/* ------------------------------------------------- the block, trained */
+/* The layer as a transformer block's second half, the norm in front of it:
+ *   h = x + resid,  y = norm(h) (fp8_add_rmsnorm_quant_1x128, bf16 stream),
+ *   out[t] = h_t + shared FFN(y_t) + sum_k gate[t, k] FFN_{idx[t, k]}(y_t)
+ * with routing on the bf16 y and the experts on the norm's own 1x128 codes.
+ *   norm_weight_dev float [H], nullable (ones);  eps > 0
+ *   x_dev, resid_dev bf16 [T, H], resid_dev nullable
+ *   h_dev      bf16 [T, H], required with resid_dev (else the residual is x)
+ *   y_dev      bf16 [T, H];  rstd_dev float [T], nullable: kept for the backward
+ * Other arguments, the workspace and its layout as moe_forward's. */
+MOE_API int moe_block_forward(const moe_config *cfg, const moe_weights *w, const float *bias_dev,
+                              const float *norm_weight_dev, float eps, const void *x_dev, const void *resid_dev,
+                              int64_t T, void *h_dev, void *y_dev, float *rstd_dev, void *out_dev, int32_t out_dtype,
+                              int32_t *idx_out_dev, int32_t *counts_out_dev, void *ws_dev, size_t ws_bytes,
+                              int32_t *err_flag_dev, void *stream);
+
+/* Its whole backward, the choice of experts held fixed: the experts as
+ * moe_backward, the gates' gradient (dL/dg = FFN(y) . dout, formed from the
+ * backward's own dh and h as g dL/dg = sum_c dh_c h_c per row) and the balance
+ * loss's through the router as moe_router_backward, and the norm as
+ * add_rmsnorm_backward.
+ *   h_dev, y_dev, rstd_dev  the forward's (h_dev: its x_dev without resid)
+ *   dout_dev   bf16 [T, H]
+ *   balance    nullable (see moe_router_backward)
+ *   dx_dev     dx_dtype [T, H]: the gradient of x, and of resid
+ *   dnorm_dev  float [H], nullable;  dwr_dev float [N_r, H]
+ *   dW13_dev, dW2_dev, w13t_dev .. s2t_dev, fwd_ws_dev  as moe_backward's
+ *   ws_dev     moe_block_backward_workspace_size() bytes, 256-byte aligned;
+ *              begins with moe_backward's (moe_backward_workspace_layout)
+ * T >= 1; only scale_mode MOE_SCALE_AMAX (else MOE_ERR_NOT_IMPLEMENTED). */
+MOE_API size_t moe_block_backward_workspace_size(const moe_config *cfg, int64_t T);
+MOE_API int moe_block_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13t_dev,
+                               const float *s13t_dev, const uint8_t *w2t_dev, const float *s2t_dev,
+                               const float *norm_weight_dev, const void *h_dev, const void *y_dev,
+                               const float *rstd_dev, const void *dout_dev, int64_t T,
+                               const moe_balance_grad *balance, void *dx_dev, int32_t dx_dtype, float *dnorm_dev,
+                               float *dwr_dev, float *dW13_dev, float *dW2_dev, const void *fwd_ws_dev,
+                               size_t fwd_ws_bytes, void *ws_dev, size_t ws_bytes, int32_t *err_flag_dev,
+                               void *stream);
 
 /* ------------------------------------------------------------ errors */
 /* Synchronises `stream`, copies *err_flag_dev to *host_value (nullable) and

@@ -19,6 +19,6 @@ from ._binding import (  # noqa: F401
     moe_workspace_size, new_err_flag, weights_struct, ws_view, moe_ep_row_bytes, moe_ep_dispatch, moe_ep_experts,
     moe_ep_combine, moe_transpose_weights, moe_backward, moe_backward_workspace_layout,
     fp8_add_rmsnorm_quant_1x128, add_rmsnorm_backward, moe_router_splits, moe_route_logits, moe_balance_loss,
-    moe_router_backward,
+    moe_router_backward, moe_block_forward, moe_block_backward,
 )
 from .layer import MoeLayer  # noqa: F401

@@ -47,7 +47,8 @@ EXPORTS = (
     "moe_ep_experts", "moe_ep_combine", "moe_transpose_weights", "moe_backward_workspace_size", "moe_backward",
     "moe_backward_workspace_layout", "fp8_add_rmsnorm_quant_1x128", "add_rmsnorm_backward_workspace_size",
     "add_rmsnorm_backward", "moe_router_splits", "moe_balance_loss_workspace_size", "moe_balance_loss",
-    "moe_router_backward_workspace_size", "moe_router_backward",
+    "moe_router_backward_workspace_size", "moe_router_backward", "moe_block_forward",
+    "moe_block_backward_workspace_size", "moe_block_backward",
 )
 MOE_GEMM_AUTO = 0
 MOE_GEMM_SINGLE = 1
@@ -145,11 +146,19 @@ lib.moe_router_backward_workspace_size.restype = _sz
 lib.moe_router_backward_workspace_size.argtypes = [_cfgp, _i64]
 lib.moe_router_backward.argtypes = [_cfgp, _vp, _i32, _vp, _i64, _vp, C.POINTER(MoeBalanceGrad), _vp, _vp, _vp, _vp,
                                     _i32, _vp, _vp, _sz, _vp, _vp]
+lib.moe_block_forward.argtypes = [_cfgp, C.POINTER(MoeWeights), _vp, _vp, _f32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
+                                  _vp, _vp, _vp, _sz, _vp, _vp]
+lib.moe_block_backward_workspace_size.restype = _sz
+lib.moe_block_backward_workspace_size.argtypes = [_cfgp, _i64]
+lib.moe_block_backward.argtypes = [_cfgp, C.POINTER(MoeWeights), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                   C.POINTER(MoeBalanceGrad), _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp,
+                                   _vp]
 for _name in EXPORTS:
     if _name not in ("moe_status_string", "moe_route_workspace_size", "moe_workspace_size", "moe_ep_row_bytes",
                      "moe_ep_dispatch_workspace_size", "moe_ep_experts_workspace_size",
                      "moe_backward_workspace_size", "add_rmsnorm_backward_workspace_size",
-                     "moe_balance_loss_workspace_size", "moe_router_backward_workspace_size"):
+                     "moe_balance_loss_workspace_size", "moe_router_backward_workspace_size",
+                     "moe_block_backward_workspace_size"):
         getattr(lib, _name).restype = C.c_int
 
 
@@ -666,6 +675,76 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
         1 if dx_accumulate else 0, wp, None if ws is None else _want(where, ws, "ws", _U8, None, dev),
         0 if ws is None else ws.numel(), _want(where, err, "err", _I32, None, dev)))
     return dlogits, dx, dwr
+
+
+def moe_block_forward(cfg: MoeConfig, w: dict, bias, x, resid=None, norm_weight=None, eps: float = 1e-6, h=None, y=None,
+                      rstd=None, out=None, out_dtype=MOE_DTYPE_BF16, idx_out=None, counts_out=None, ws=None, err=None,
+                      stream=None):
+    """The layer with the norm in front: h = x + resid, out = h + MoE(norm(h)).
+    Returns (out, h, y, rstd); the last three and the workspace are what
+    moe_block_backward reads.  w as moe_forward's."""
+    where = "moe_block_forward"
+    idx = _cuda_index(where, x, "x")
+    if x.dim() != 2 or x.shape[1] != cfg.hidden:
+        _refuse(where, f"x is {tuple(x.shape)}, wanted [T, {cfg.hidden}]")
+    shape, T, H, dev, cp = x.shape, x.shape[0], cfg.hidden, x.device, C.byref(cfg)
+    if resid is not None and h is None:
+        h = torch.empty(shape, dtype=_BF16, device=dev)
+    y = torch.empty(shape, dtype=_BF16, device=dev) if y is None else y
+    rstd = torch.empty((T,), dtype=_F32, device=dev) if rstd is None else rstd
+    odt = _F32 if out_dtype == MOE_DTYPE_F32 else _BF16
+    out = torch.empty(shape, dtype=odt, device=dev) if out is None else out
+    ws = _scratch(lib.moe_workspace_size, idx, cp, T) if ws is None else ws
+    err = new_err_flag(dev) if err is None else err
+    wst = weights_struct(w)
+    _on_device(lib.moe_block_forward, idx, stream, where, (
+        cp, C.byref(wst), _want(where, bias, "bias", _F32, (cfg.n_routed,), idx),
+        None if norm_weight is None else _want(where, norm_weight, "norm_weight", _F32, (H,), idx), eps,
+        _want(where, x, "x", _BF16, shape, idx),
+        None if resid is None else _want(where, resid, "resid", _BF16, shape, idx), T,
+        None if h is None else _want(where, h, "h", _BF16, shape, idx), _want(where, y, "y", _BF16, shape, idx),
+        _want(where, rstd, "rstd", _F32, (T,), idx), _want(where, out, "out", odt, shape, idx), out_dtype,
+        None if idx_out is None else _want(where, idx_out, "idx_out", _I32, (T, cfg.top_k), idx),
+        None if counts_out is None else _want(where, counts_out, "counts_out", _I32, (cfg.n_routed,), idx),
+        _want(where, ws, "ws", _U8, None, idx), ws.numel(), _want(where, err, "err", _I32, None, idx)))
+    return out, x if h is None else h, y, rstd
+
+
+def moe_block_backward(cfg: MoeConfig, w: dict, wt: dict, h, y, rstd, dout, fwd_ws, norm_weight=None, balance=None,
+                       dx=None, dnorm=None, dwr=None, dW13=None, dW2=None, dx_dtype=None, ws=None, err=None,
+                       stream=None):
+    """Every gradient of moe_block_forward for the batch whose forward left
+    its state in fwd_ws: (dx [T, H] bf16 (or dx_dtype), dnorm [H], dwr [N_r,
+    H], dW13 [E, 2I, H], dW2 [E, H, I]).  balance: as moe_router_backward's."""
+    where = "moe_block_backward"
+    idx = _cuda_index(where, h, "h")
+    if h.dim() != 2 or h.shape[1] != cfg.hidden:
+        _refuse(where, f"h is {tuple(h.shape)}, wanted [T, {cfg.hidden}]")
+    shape, T, H, dev, cp = h.shape, h.shape[0], cfg.hidden, h.device, C.byref(cfg)
+    E, I, Nr = cfg.n_routed + cfg.n_shared, cfg.inter, cfg.n_routed
+    if dx is None:
+        dx = torch.empty(shape, dtype=dx_dtype or _BF16, device=dev)
+    elif dx_dtype is not None and dx.dtype is not dx_dtype:
+        _refuse(where, f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+    code = _stream_type(where, dx, "dx")
+    dnorm = torch.empty((H,), dtype=_F32, device=dev) if dnorm is None else dnorm
+    dwr = torch.empty((Nr, H), dtype=_F32, device=dev) if dwr is None else dwr
+    dW13 = torch.empty((E, 2 * I, H), dtype=_F32, device=dev) if dW13 is None else dW13
+    dW2 = torch.empty((E, H, I), dtype=_F32, device=dev) if dW2 is None else dW2
+    ws = _scratch(lib.moe_block_backward_workspace_size, idx, cp, T) if ws is None else ws
+    err = new_err_flag(dev) if err is None else err
+    wst = weights_struct(w)
+    _on_device(lib.moe_block_backward, idx, stream, where, (
+        cp, C.byref(wst), _ptr(wt["w13t"]), _ptr(wt["s13t"]), _ptr(wt["w2t"]), _ptr(wt["s2t"]),
+        None if norm_weight is None else _want(where, norm_weight, "norm_weight", _F32, (H,), idx),
+        _want(where, h, "h", _BF16, shape, idx), _want(where, y, "y", _BF16, shape, idx),
+        _want(where, rstd, "rstd", _F32, (T,), idx), _want(where, dout, "dout", _BF16, shape, idx), T,
+        None if balance is None else C.byref(_balance_struct(where, cfg, balance, idx)),
+        _want(where, dx, "dx", dx.dtype, shape, idx), code, _want(where, dnorm, "dnorm", _F32, (H,), idx),
+        _want(where, dwr, "dwr", _F32, (Nr, H), idx), _want(where, dW13, "dW13", _F32, (E, 2 * I, H), idx),
+        _want(where, dW2, "dW2", _F32, (E, H, I), idx), _want(where, fwd_ws, "fwd_ws", _U8, None, idx), fwd_ws.numel(),
+        _want(where, ws, "ws", _U8, None, idx), ws.numel(), _want(where, err, "err", _I32, None, idx)))
+    return dx, dnorm, dwr, dW13, dW2
 
 
 def ws_view(ws: torch.Tensor, layout: dict, name: str, dtype, shape) -> torch.Tensor:

@@ -571,34 +571,29 @@ static cudaError_t run_expert_path(const ExpertPath &P) {
   return e;
 }
 
-int moe_forward(const moe_config *cfg, const moe_weights *w, const float *bias, const void *x, int64_t T, void *out,
-                int32_t out_dtype, int32_t *idx_out, int32_t *counts_out, void *ws, size_t ws_bytes,
-                int32_t *err_flag, void *stream) {
-  const NvtxRange nvtx_call("moe_forward");
-  if (const int c = check_cfg(cfg)) return c;
-  if (T < 0 || T > kMaxTokens) return MOE_ERR_INVALID_ARG;
-  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T == 0) {
-    if (counts_out) {
-      if (const int d = check_device()) return d;
-      return cuda_status(cudaMemsetAsync(counts_out, 0, sizeof(int32_t) * cfg->n_routed, st));
-    }
-    return MOE_OK;
-  }
-  if (!w || !bias || !x || !out || !ws || !err_flag) return MOE_ERR_INVALID_ARG;
+// The arguments that moe_forward and moe_block_forward share; *L gets the
+// workspace's layout.
+static int check_forward(const moe_config *cfg, const moe_weights *w, const float *bias, const void *out,
+                         const int32_t *idx_out, const int32_t *counts_out, int64_t T, const void *ws, size_t ws_bytes,
+                         const int32_t *err_flag, moe_ws_layout *L) {
+  if (!w || !bias || !out || !ws || !err_flag) return MOE_ERR_INVALID_ARG;
   if (!w->w13_dev || !w->s13_dev || !w->w2_dev || !w->s2_dev || !w->wr_dev) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(out) || !aligned16(w->w13_dev) || !aligned16(w->w2_dev) || !aligned16(w->wr_dev) ||
+  if (!aligned16(out) || !aligned16(w->w13_dev) || !aligned16(w->w2_dev) || !aligned16(w->wr_dev) ||
       (reinterpret_cast<uintptr_t>(ws) & 255))
     return MOE_ERR_INVALID_ARG;
   if (!aligned4(w->s13_dev) || !aligned4(w->s2_dev) || !aligned4(bias) || !aligned4(err_flag) ||
       !aligned4(idx_out) || !aligned4(counts_out))
     return MOE_ERR_INVALID_ARG;
-  moe_ws_layout L;
-  make_layout(cfg, T, &L);
-  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (const int d = check_device()) return d;
+  make_layout(cfg, T, L);
+  return ws_bytes < L->total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
 
+// A forward behind the quantization of the experts' input into ws (xq, xs):
+// routing on u, the experts, the combine onto the residual `resid`.
+static cudaError_t run_routed(const moe_config *cfg, const moe_weights *w, const float *bias, const void *u,
+                              const void *resid, int64_t T, void *out, int32_t out_dtype, int32_t *idx_out,
+                              int32_t *counts_out, const moe_ws_layout &L, void *ws, int32_t *err_flag,
+                              cudaStream_t st) {
   const int H = cfg->hidden, Nr = cfg->n_routed, Kr = cfg->top_k;
   uint8_t *xq = at<uint8_t *>(ws, L.xq);
   float *xs = at<float *>(ws, L.xs);
@@ -606,13 +601,7 @@ int moe_forward(const moe_config *cfg, const moe_weights *w, const float *bias, 
   float *gate = at<float *>(ws, L.gate);
   float *logits = at<float *>(ws, L.logits);
   const int ks = moe::router_ksplit(T, Nr, H);
-
-  cudaError_t e = prof_mark(0, st);
-  const bool pow2 = cfg->scale_mode == MOE_SCALE_POW2;
-  if (e == cudaSuccess) e = moe::launch_quant_1x128(x, T, H, H, xq, xs, st, pow2);
-  if (e == cudaSuccess) e = prof_mark(1, st);
-  if (e == cudaSuccess)
-    e = moe::launch_router_logits(x, w->wr_dev, T, Nr, H, logits, err_flag, moe::kDefaultWaitLimitNs, st);
+  cudaError_t e = moe::launch_router_logits(u, w->wr_dev, T, Nr, H, logits, err_flag, moe::kDefaultWaitLimitNs, st);
   if (e == cudaSuccess)
     e = moe::launch_router_topk(logits, ks, T, Nr, Kr, cfg->n_groups, cfg->topk_groups, cfg->route_scale, bias,
                                 idx, gate, nullptr, st);
@@ -628,7 +617,7 @@ int moe_forward(const moe_config *cfg, const moe_weights *w, const float *bias, 
     P.idx = idx;
     P.gate = gate;
     P.allow_empty = 0;
-    P.x_resid = x;
+    P.x_resid = resid;
     P.out = out;
     P.out_f32 = out_dtype == MOE_DTYPE_F32;
     P.counts_out = counts_out;
@@ -640,6 +629,69 @@ int moe_forward(const moe_config *cfg, const moe_weights *w, const float *bias, 
   }
   if (e == cudaSuccess && idx_out)
     e = cudaMemcpyAsync(idx_out, idx, sizeof(int32_t) * T * Kr, cudaMemcpyDeviceToDevice, st);
+  return e;
+}
+
+int moe_forward(const moe_config *cfg, const moe_weights *w, const float *bias, const void *x, int64_t T, void *out,
+                int32_t out_dtype, int32_t *idx_out, int32_t *counts_out, void *ws, size_t ws_bytes,
+                int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_forward");
+  if (const int c = check_cfg(cfg)) return c;
+  if (T < 0 || T > kMaxTokens) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (counts_out) {
+      if (const int d = check_device()) return d;
+      return cuda_status(cudaMemsetAsync(counts_out, 0, sizeof(int32_t) * cfg->n_routed, st));
+    }
+    return MOE_OK;
+  }
+  if (!x || !aligned16(x)) return MOE_ERR_INVALID_ARG;
+  moe_ws_layout L;
+  if (const int c = check_forward(cfg, w, bias, out, idx_out, counts_out, T, ws, ws_bytes, err_flag, &L)) return c;
+  if (const int d = check_device()) return d;
+  const int H = cfg->hidden;
+  cudaError_t e = prof_mark(0, st);
+  if (e == cudaSuccess)
+    e = moe::launch_quant_1x128(x, T, H, H, at<uint8_t *>(ws, L.xq), at<float *>(ws, L.xs), st,
+                                cfg->scale_mode == MOE_SCALE_POW2);
+  if (e == cudaSuccess) e = prof_mark(1, st);
+  if (e == cudaSuccess)
+    e = run_routed(cfg, w, bias, x, x, T, out, out_dtype, idx_out, counts_out, L, ws, err_flag, st);
+  return cuda_status(e);
+}
+
+int moe_block_forward(const moe_config *cfg, const moe_weights *w, const float *bias, const float *norm_weight,
+                      float eps, const void *x, const void *resid, int64_t T, void *h, void *y, float *rstd, void *out,
+                      int32_t out_dtype, int32_t *idx_out, int32_t *counts_out, void *ws, size_t ws_bytes,
+                      int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_block_forward");
+  if (const int c = check_cfg(cfg)) return c;
+  if (T < 0 || T > kMaxTokens || !(eps > 0.0f) || eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (counts_out) {
+      if (const int d = check_device()) return d;
+      return cuda_status(cudaMemsetAsync(counts_out, 0, sizeof(int32_t) * cfg->n_routed, st));
+    }
+    return MOE_OK;
+  }
+  if (!x || !y || (resid && !h)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(resid) || !aligned16(norm_weight) || !aligned16(h) || !aligned16(y) || !aligned4(rstd))
+    return MOE_ERR_INVALID_ARG;
+  moe_ws_layout L;
+  if (const int c = check_forward(cfg, w, bias, out, idx_out, counts_out, T, ws, ws_bytes, err_flag, &L)) return c;
+  if (const int d = check_device()) return d;
+  const int H = cfg->hidden;
+  cudaError_t e = prof_mark(0, st);
+  if (e == cudaSuccess)
+    e = moe::launch_add_rmsnorm_quant(x, H, resid, H, false, norm_weight, eps, T, H, h, y, at<uint8_t *>(ws, L.xq),
+                                      at<float *>(ws, L.xs), rstd, cfg->scale_mode == MOE_SCALE_POW2, st);
+  if (e == cudaSuccess) e = prof_mark(1, st);
+  if (e == cudaSuccess)
+    e = run_routed(cfg, w, bias, y, resid ? h : x, T, out, out_dtype, idx_out, counts_out, L, ws, err_flag, st);
   return cuda_status(e);
 }
 
@@ -855,29 +907,14 @@ size_t moe_backward_workspace_size(const moe_config *cfg, int64_t T) {
   return B.total;
 }
 
-int moe_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13t, const float *s13t,
-                 const uint8_t *w2t, const float *s2t, const void *x, const void *dout, int64_t T, float *dx,
-                 float *dW13, float *dW2, const void *fwd_ws, size_t fwd_ws_bytes, void *ws, size_t ws_bytes,
-                 int32_t *err_flag, void *stream) {
-  const NvtxRange nvtx_call("moe_backward");
-  if (const int c = check_cfg(cfg)) return c;
-  if (cfg->scale_mode != MOE_SCALE_AMAX) return MOE_ERR_NOT_IMPLEMENTED;
-  if (T < 1 || T > kMaxTokens) return MOE_ERR_INVALID_ARG;
-  if (!w || !w->w13_dev || !w->s13_dev || !w->w2_dev || !w->s2_dev || !w13t || !s13t || !w2t || !s2t || !x ||
-      !dout || !dx || !dW13 || !dW2 || !fwd_ws || !ws || !err_flag)
-    return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(dout) || !aligned16(dx) || !aligned16(dW13) || !aligned16(dW2) ||
-      !aligned16(w13t) || !aligned16(w2t) || !aligned4(s13t) || !aligned4(s2t) || !aligned4(err_flag) ||
-      (reinterpret_cast<uintptr_t>(ws) & 255) || (reinterpret_cast<uintptr_t>(fwd_ws) & 255))
-    return MOE_ERR_INVALID_ARG;
-  moe_ws_layout L;
-  make_layout(cfg, T, &L);
-  if (fwd_ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  BwdLayout B;
-  make_bwd_layout(cfg, T, &B);
-  if (ws_bytes < B.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (const int d = check_device()) return d;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+// The launches of the experts' backward.  base: what dx starts from (dout for
+// the layer's own residual, null for none); gdot: see swiglu_bwd_kernel (null:
+// not wanted).
+static cudaError_t run_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13t, const float *s13t,
+                                const uint8_t *w2t, const float *s2t, const void *x, const void *dout,
+                                const void *base, int64_t T, float *dx, float *dW13, float *dW2, float *gdot,
+                                const void *fwd_ws, const moe_ws_layout &L, void *ws, const BwdLayout &B,
+                                int32_t *err_flag, cudaStream_t st) {
   void *fws = const_cast<void *>(fwd_ws);
   const int H = cfg->hidden, I = cfg->inter, Nr = cfg->n_routed, Kr = cfg->top_k, Ns = cfg->n_shared;
   const int64_t R = T * Kr, RS = R + T * Ns, E = static_cast<int64_t>(Nr) + Ns;
@@ -980,7 +1017,7 @@ int moe_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13
     e = moe::launch_gemm(g, st);
   }
   if (e == cudaSuccess) e = prof_mark_bwd(2, st);
-  if (e == cudaSuccess) e = moe::launch_swiglu_bwd(GU, dh, row_gate, RS, I, ghbuf, dGU, dGUq, dGUs, pitch, st);
+  if (e == cudaSuccess) e = moe::launch_swiglu_bwd(GU, dh, row_gate, RS, I, ghbuf, dGU, dGUq, dGUs, pitch, st, gdot);
   if (e == cudaSuccess) e = prof_mark_bwd(3, st);
   if (e == cudaSuccess) {
     // dx rows = [dG|dU] [W1; W3] (FP32): K = 2I against W13^T [E, H, 2I]
@@ -1007,9 +1044,9 @@ int moe_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13
     g.out_cols = H;
     e = moe::launch_gemm(g, st);
   }
-  // dx_t = dout_t + the token's rows (shared, then its slots), FP32
+  // dx_t = base_t (if given) + the token's rows (shared, then its slots), FP32
   if (e == cudaSuccess) e = prof_mark_bwd(4, st);
-  if (e == cudaSuccess) e = moe::launch_combine(dout, dxr, pos, T, H, Kr, R, Ns, dx, 1, st, true);
+  if (e == cudaSuccess) e = moe::launch_combine(base, dxr, pos, T, H, Kr, R, Ns, dx, 1, st, true);
   if (e == cudaSuccess) e = prof_mark_bwd(5, st);
   // weight gradients: 128-token tiles of every expert, operands transposed
   if (e == cudaSuccess) e = moe::launch_wgrad_tiles(offsets, Nr, Ns, R, T, seg, tiles, tmeta, st);
@@ -1061,7 +1098,33 @@ int moe_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13
     e = moe::launch_gemm_wgrad(g, st);
   }
   if (e == cudaSuccess) e = prof_mark_bwd(8, st);
-  return cuda_status(e);
+  return e;
+}
+
+int moe_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13t, const float *s13t,
+                 const uint8_t *w2t, const float *s2t, const void *x, const void *dout, int64_t T, float *dx,
+                 float *dW13, float *dW2, const void *fwd_ws, size_t fwd_ws_bytes, void *ws, size_t ws_bytes,
+                 int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_backward");
+  if (const int c = check_cfg(cfg)) return c;
+  if (cfg->scale_mode != MOE_SCALE_AMAX) return MOE_ERR_NOT_IMPLEMENTED;
+  if (T < 1 || T > kMaxTokens) return MOE_ERR_INVALID_ARG;
+  if (!w || !w->w13_dev || !w->s13_dev || !w->w2_dev || !w->s2_dev || !w13t || !s13t || !w2t || !s2t || !x ||
+      !dout || !dx || !dW13 || !dW2 || !fwd_ws || !ws || !err_flag)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(dout) || !aligned16(dx) || !aligned16(dW13) || !aligned16(dW2) ||
+      !aligned16(w13t) || !aligned16(w2t) || !aligned4(s13t) || !aligned4(s2t) || !aligned4(err_flag) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255) || (reinterpret_cast<uintptr_t>(fwd_ws) & 255))
+    return MOE_ERR_INVALID_ARG;
+  moe_ws_layout L;
+  make_layout(cfg, T, &L);
+  if (fwd_ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  BwdLayout B;
+  make_bwd_layout(cfg, T, &B);
+  if (ws_bytes < B.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int d = check_device()) return d;
+  return cuda_status(run_backward(cfg, w, w13t, s13t, w2t, s2t, x, dout, dout, T, dx, dW13, dW2, nullptr, fwd_ws, L, ws,
+                                  B, err_flag, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_seq_balance_loss(const moe_config *cfg, int64_t T, int64_t seq_len, float alpha, const void *ws,
@@ -1255,6 +1318,98 @@ int moe_router_backward(const moe_config *cfg, const float *logits, int32_t n_sp
   g.err = err_flag;
   return cuda_status(
       run_router_bwd(cfg, g, x, wr, dx, dx_accumulate, dwr, ws, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// The block's backward workspace: the experts' backward first, then the
+// gradient of the norm's output, the gates' row sums, the router's and the
+// norm's scratch.
+struct BlockBwdLayout {
+  BwdLayout B;
+  size_t dy[2], gdot[2], router[2], norm[2], total;
+};
+void make_block_bwd_layout(const moe_config *c, int64_t T, BlockBwdLayout *L) {
+  make_bwd_layout(c, T, &L->B);
+  const int64_t rows = T * (c->top_k + c->n_shared);
+  RouterBwdLayout r;
+  make_router_bwd_layout(c, T, &r);
+  Carve cv;
+  cv.off = L->B.total;
+  cv.take(L->dy, T * c->hidden * 4);
+  cv.take(L->gdot, rows * (c->inter / 128) * 4);
+  cv.take(L->router, r.total);
+  cv.take(L->norm, add_rmsnorm_backward_workspace_size(T, c->hidden));
+  L->total = (cv.off + 255) & ~size_t(255);
+}
+}  // namespace
+
+size_t moe_block_backward_workspace_size(const moe_config *cfg, int64_t T) {
+  if (check_cfg(cfg) != MOE_OK || T < 0 || T > kMaxTokens) return 0;
+  BlockBwdLayout L;
+  make_block_bwd_layout(cfg, T, &L);
+  return L.total;
+}
+
+int moe_block_backward(const moe_config *cfg, const moe_weights *w, const uint8_t *w13t, const float *s13t,
+                       const uint8_t *w2t, const float *s2t, const float *norm_weight, const void *h, const void *y,
+                       const float *rstd, const void *dout, int64_t T, const moe_balance_grad *balance, void *dx,
+                       int32_t dx_dtype, float *dnorm, float *dwr, float *dW13, float *dW2, const void *fwd_ws,
+                       size_t fwd_ws_bytes, void *ws, size_t ws_bytes, int32_t *err_flag, void *stream) {
+  const NvtxRange nvtx_call("moe_block_backward");
+  if (const int c = check_cfg(cfg)) return c;
+  if (cfg->scale_mode != MOE_SCALE_AMAX) return MOE_ERR_NOT_IMPLEMENTED;
+  if (T < 1 || T > kMaxTokens || !dtype_ok(dx_dtype)) return MOE_ERR_INVALID_ARG;
+  if (balance)
+    if (const int c = check_balance(balance)) return c;
+  if (!w || !w->w13_dev || !w->s13_dev || !w->w2_dev || !w->s2_dev || !w->wr_dev || !w13t || !s13t || !w2t || !s2t ||
+      !h || !y || !rstd || !dout || !dx || !dwr || !dW13 || !dW2 || !fwd_ws || !ws || !err_flag)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(norm_weight) || !aligned16(h) || !aligned16(y) || !aligned4(rstd) || !aligned16(dout) ||
+      !aligned16(dx) || !aligned4(dnorm) || !aligned16(dwr) || !aligned16(dW13) || !aligned16(dW2) ||
+      !aligned16(w->wr_dev) || !aligned16(w13t) || !aligned16(w2t) || !aligned4(s13t) || !aligned4(s2t) ||
+      !aligned4(err_flag) || (reinterpret_cast<uintptr_t>(ws) & 255) || (reinterpret_cast<uintptr_t>(fwd_ws) & 255))
+    return MOE_ERR_INVALID_ARG;
+  moe_ws_layout F;
+  make_layout(cfg, T, &F);
+  if (fwd_ws_bytes < F.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  BlockBwdLayout L;
+  make_block_bwd_layout(cfg, T, &L);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int d = check_device()) return d;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void *fws = const_cast<void *>(fwd_ws);
+  float *dy = at<float *>(ws, L.dy), *gdot = at<float *>(ws, L.gdot);
+  // the experts: dy = F^T dout, without the residual's share
+  cudaError_t e = run_backward(cfg, w, w13t, s13t, w2t, s2t, y, dout, nullptr, T, dy, dW13, dW2, gdot, fwd_ws, F, ws,
+                               L.B, err_flag, st);
+  if (e == cudaSuccess) {
+    // the router adds its share to dy
+    moe::RouterBwd g{};
+    g.partial = at<float *>(fws, F.logits);
+    g.n_ks = moe::router_ksplit(T, cfg->n_routed, cfg->hidden);
+    g.T = T;
+    g.Nr = cfg->n_routed;
+    g.Kr = cfg->top_k;
+    g.route_scale = cfg->route_scale;
+    g.idx = at<int32_t *>(fws, F.idx);
+    g.gdot = gdot;
+    g.pos = at<int32_t *>(fws, F.pos);
+    g.n_dot = cfg->inter / 128;
+    if (balance && balance->n_seq > 0) {
+      g.off = balance->seq_offsets_dev;
+      g.n_seq = balance->n_seq;
+      g.counts = balance->counts_dev;
+      g.dloss = balance->dloss_dev;
+      g.alpha = balance->alpha;
+    }
+    g.err = err_flag;
+    e = run_router_bwd(cfg, g, y, w->wr_dev, dy, 1, dwr, static_cast<uint8_t *>(ws) + L.router[0], st);
+  }
+  // the norm, and the residual's share dout
+  if (e == cudaSuccess)
+    e = moe::launch_add_rmsnorm_bwd(dy, true, h, dout, false, norm_weight, rstd, T, cfg->hidden, dx,
+                                    dx_dtype == MOE_DTYPE_F32, dnorm, at<float *>(ws, L.norm), st);
+  return cuda_status(e);
 }
 
 int moe_profile_events(void *const *events, int32_t n_events) {

@@ -137,12 +137,16 @@ __global__ void __launch_bounds__(256) dout_quant_kernel(const uint16_t *__restr
 //   dG = dh U sig (1 + G (1 - sig)), dU = dh silu          (FP32)
 // Writes gh = g h [RS, I] (the dW2 operand) and dGU [RS, 2I] (dG at column
 // c, dU at I + c) in FP32, and dG | dU quantized 1x128 along I: codes
-// [RS, 2I], scales into the transposed table [2I/128][ld].
+// [RS, 2I], scales into the transposed table [2I/128][ld].  With gdot
+// [RS, I/128] also this group's share of the row's g dL/dg = sum_c dh h (dh
+// carries g, so nothing is divided by a gate that may be 0); the router's
+// backward adds a row's shares in order.
 __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const float *__restrict__ GU, const float *__restrict__ dh,
                                                           const float *__restrict__ row_gate, int64_t RS, int I,
                                                           float *__restrict__ h,
                                                           float *__restrict__ dGU, uint8_t *__restrict__ q,
-                                                          float *__restrict__ s_t, int64_t ld) {
+                                                          float *__restrict__ s_t, int64_t ld,
+                                                          float *__restrict__ gdot) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t groups = I / 128;
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const float *__restrict
   const float G[4] = {G4.x, G4.y, G4.z, G4.w}, U[4] = {U4.x, U4.y, U4.z, U4.w}, D[4] = {D4.x, D4.y, D4.z, D4.w};
   const float gt = __ldg(row_gate + p);
   float hv[4], dg[4], du[4];
-  float ag = 0.0f, au = 0.0f;
+  float ag = 0.0f, au = 0.0f, dot = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float sig = 1.0f / (1.0f + expf(-G[i]));
@@ -163,6 +167,7 @@ __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const float *__restrict
     hv[i] = gt * (silu * U[i]);
     dg[i] = D[i] * U[i] * sig * (1.0f + G[i] * (1.0f - sig));
     du[i] = D[i] * silu;
+    dot = fmaf(D[i], silu * U[i], dot);
     ag = fmaxf(ag, fabsf(dg[i]));
     au = fmaxf(au, fabsf(du[i]));
   }
@@ -173,6 +178,11 @@ __global__ void __launch_bounds__(256) swiglu_bwd_kernel(const float *__restrict
   for (int o = 16; o > 0; o >>= 1) {
     ag = fmaxf(ag, __shfl_xor_sync(0xffffffffu, ag, o));
     au = fmaxf(au, __shfl_xor_sync(0xffffffffu, au, o));
+  }
+  if (gdot) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) gdot[p * groups + j] = dot;
   }
   const float Sg = ag / 448.0f, Su = au / 448.0f;
   uint32_t wg = 0, wu = 0;
@@ -351,11 +361,12 @@ cudaError_t launch_dout_quant(const void *dout, const int32_t *row_src, int64_t 
 }
 
 cudaError_t launch_swiglu_bwd(const float *GU, const float *dh, const float *row_gate, int64_t RS, int I, float *h,
-                              float *dGU, uint8_t *q, float *s_t, int64_t ld, cudaStream_t st) {
+                              float *dGU, uint8_t *q, float *s_t, int64_t ld, cudaStream_t st, float *gdot) {
   const int64_t warps = RS * (I / 128);
   if (warps == 0) return cudaSuccess;
   const int64_t blocks = (warps + 7) / 8;
-  swiglu_bwd_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(GU, dh, row_gate, RS, I, h, dGU, q, s_t, ld);
+  swiglu_bwd_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(GU, dh, row_gate, RS, I, h, dGU, q, s_t, ld,
+                                                                  gdot);
   return cudaGetLastError();
 }
 

@@ -196,7 +196,7 @@ cudaError_t launch_transpose_blocks(const uint8_t *q, const float *s, int64_t n,
 cudaError_t launch_dout_quant(const void *dout, const int32_t *row_src, int64_t R, int64_t RS, int H, uint8_t *q,
                               float *s_t, int64_t ld, cudaStream_t st);
 cudaError_t launch_swiglu_bwd(const float *GU, const float *dh, const float *row_gate, int64_t RS, int I, float *h,
-                              float *dGU, uint8_t *q, float *s_t, int64_t ld, cudaStream_t st);
+                              float *dGU, uint8_t *q, float *s_t, int64_t ld, cudaStream_t st, float *gdot = nullptr);
 cudaError_t launch_wgrad_tiles(const int32_t *offsets, int Nr, int Ns, int64_t R, int64_t T, int32_t *seg,
                                int4 *tiles, int32_t *meta, cudaStream_t st);
 // src: 0 = FP32 rows (f32rows, f32_ld floats apart), 1 = bf16 [T, C] rows

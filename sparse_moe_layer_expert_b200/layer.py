@@ -137,6 +137,58 @@ class MoeLayer:
             bws[T] = ws
         return ws
 
+    # ---------------------------------------------- the block: norm + layer
+    def block_forward(self, x: torch.Tensor, resid=None, norm_weight=None, eps: float = 1e-6, out=None,
+                      out_dtype=B.MOE_DTYPE_BF16, idx_out=None, counts_out=None, stream=None):
+        """h = x + resid, out = h + MoE(rmsnorm(h) * norm_weight): (out,
+        saved).  `saved` is what block_backward takes; the routing and the
+        experts' state stay in this layer's workspace for that batch size, so
+        the backward has to come before its next forward of the same size."""
+        T = x.shape[0]
+        out, h, y, rstd = B.moe_block_forward(self.cfg, self.weights(), self.bias, x, resid, norm_weight, eps, out=out,
+                                              out_dtype=out_dtype, idx_out=idx_out, counts_out=counts_out,
+                                              ws=self.workspace(T), err=self.err, stream=stream)
+        return out, dict(h=h, y=y, rstd=rstd, norm_weight=norm_weight)
+
+    def router_state(self, T: int):
+        """(logit partials [n_splits, T, N_r], picks [T, K_r]) that this
+        layer's last forward of T tokens left in its workspace (views)."""
+        L = self.layout(T)
+        ws, Nr = self.workspace(T), self.cfg.n_routed
+        n = L["logits"][1] // (T * Nr * 4) if T else 1
+        return (B.ws_view(ws, L, "logits", torch.float32, (n, T, Nr)),
+                B.ws_view(ws, L, "idx", torch.int32, (T, self.cfg.top_k)))
+
+    def balance_loss(self, T: int, seq_offsets: torch.Tensor, alpha: float = 1e-4, stream=None):
+        """Balance loss and per-expert counts of the packed sequences of the
+        batch this layer's last forward of T tokens routed: (loss, grad), grad
+        being what block_backward takes as `balance` (dloss: ones)."""
+        logits, idx = self.router_state(T)
+        loss, counts = B.moe_balance_loss(self.cfg, logits, idx, seq_offsets, alpha=alpha, err=self.err, stream=stream)
+        return loss, dict(seq_offsets=seq_offsets, counts=counts, alpha=alpha)
+
+    def block_backward(self, saved: dict, dout: torch.Tensor, balance=None, dx_dtype=None, stream=None) -> dict:
+        """Gradients of block_forward's batch: dict(dx (of x and of resid),
+        dnorm, dwr, dW13, dW2)."""
+        if getattr(self, "_wt", None) is None:
+            self._wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
+        T = dout.shape[0]
+        g = B.moe_block_backward(self.cfg, self.weights(), self._wt, saved["h"], saved["y"], saved["rstd"], dout,
+                                 self.workspace(T), norm_weight=saved["norm_weight"], balance=balance,
+                                 dx_dtype=dx_dtype, ws=self.block_backward_workspace(T), err=self.err, stream=stream)
+        return dict(zip(("dx", "dnorm", "dwr", "dW13", "dW2"), g))
+
+    def block_backward_workspace(self, T: int) -> torch.Tensor:
+        bws = getattr(self, "_bbws", None)
+        if bws is None:
+            bws = self._bbws = {}
+        ws = bws.get(T)
+        if ws is None:
+            ws = torch.empty(max(int(B.lib.moe_block_backward_workspace_size(B.ctypes_cfg(self.cfg), T)), 256),
+                             dtype=torch.uint8, device=self.device)
+            bws[T] = ws
+        return ws
+
     def check(self, stream=None) -> None:
         st, v = B.moe_check_device_error(self.err, stream)
         if st != B.MOE_OK:

@@ -118,3 +118,42 @@ def test_bindings_refuse_host_tensors(m):
                            torch.zeros(2, dtype=torch.int32))
     with pytest.raises(m.MoeError):
         m.moe_router_backward(cfg, torch.zeros((1, 2, 16)), torch.zeros((2, 4), dtype=torch.int32), dlogits=True)
+
+
+def test_block_refusals(m):
+    cfg = m.config(512, 256, 16, 4)
+    w = m._binding.MoeWeights(16, 16, 16, 16, 16)
+    need = m.moe_workspace_size(cfg, 64)
+    ok = dict(cfg=C.byref(cfg), w=C.byref(w), bias=16, nw=None, eps=1e-6, x=16, r=None, T=64, h=None, y=16, rstd=None,
+              out=16, od=0, idx=None, cnt=None, ws=256, wb=need, err=16)
+
+    def fwd(**kw):
+        a = {**ok, **kw}
+        return m.lib.moe_block_forward(*[a[k] for k in ok], None)
+
+    assert fwd() == m.MOE_ERR_NO_DEVICE and fwd(r=16, h=32) == m.MOE_ERR_NO_DEVICE
+    assert fwd(T=0) == m.MOE_OK
+    assert fwd(wb=need - 1) == m.MOE_ERR_WORKSPACE_TOO_SMALL
+    for bad in (dict(cfg=None), dict(w=None), dict(bias=None), dict(eps=0.0), dict(x=None), dict(y=None), dict(r=16),
+                dict(T=-1), dict(od=3), dict(out=None), dict(ws=128), dict(err=None), dict(nw=20), dict(y=24),
+                dict(rstd=18), dict(h=24)):
+        assert fwd(**bad) == m.MOE_ERR_INVALID_ARG, bad
+
+    need_b = m.lib.moe_block_backward_workspace_size(C.byref(cfg), 64)
+    assert need_b > m.lib.moe_backward_workspace_size(C.byref(cfg), 64)
+    okb = dict(cfg=C.byref(cfg), w=C.byref(w), a=16, b=16, c=16, d=16, nw=None, h=16, y=16, rstd=16, dout=16, T=64,
+               bal=None, dx=16, dxt=0, dn=None, dwr=16, dW13=16, dW2=16, f=256, fb=need, ws=256, wb=need_b, err=16)
+
+    def bwd(**kw):
+        a = {**okb, **kw}
+        return m.lib.moe_block_backward(*[a[k] for k in okb], None)
+
+    assert bwd() == m.MOE_ERR_NO_DEVICE
+    assert bwd(wb=need_b - 1) == m.MOE_ERR_WORKSPACE_TOO_SMALL and bwd(fb=need - 1) == m.MOE_ERR_WORKSPACE_TOO_SMALL
+    p2 = m.config(512, 256, 16, 4, scale_mode=m.MOE_SCALE_POW2)
+    assert bwd(cfg=C.byref(p2)) == m.MOE_ERR_NOT_IMPLEMENTED
+    bal = m._binding.MoeBalanceGrad(16, 2, 1e-4, None, None)
+    for bad in (dict(T=0), dict(h=None), dict(y=None), dict(rstd=None), dict(dout=None), dict(dx=None), dict(dwr=None),
+                dict(dW13=None), dict(f=None), dict(ws=128), dict(err=None), dict(dxt=2), dict(dx=24), dict(nw=20),
+                dict(bal=C.byref(bal))):
+        assert bwd(**bad) == m.MOE_ERR_INVALID_ARG, bad
