@@ -67,12 +67,96 @@ __device__ __forceinline__ void load8_sh(const float *p, float (&f)[8]) {
   f[0] = up ? b.x : a.x, f[1] = up ? b.y : a.y, f[2] = up ? b.z : a.z, f[3] = up ? b.w : a.w;
   f[4] = up ? a.x : b.x, f[5] = up ? a.y : b.y, f[6] = up ? a.z : b.z, f[7] = up ? a.w : b.w;
 }
-// h rounded to the stream's type (the value later readers of h see)
-__device__ __forceinline__ void round8(const __nv_bfloat16 *, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
+// Two FP32 operations an instruction, each rounded to nearest.
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+  uint64_t a, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
-__device__ __forceinline__ void round8(const float *, float (&)[8]) {}
+__device__ __forceinline__ void mul8(float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) mul2(a[i], a[i + 1], b[i], b[i + 1]);
+}
+__device__ __forceinline__ void mul8(float (&a)[8], float b) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) mul2(a[i], a[i + 1], b, b);
+}
+
+// One chunk of h = x + resid, rounded to the stream's type, in FP32; and the
+// chunk as it is stored.  In bf16 the packed addition rounds the exact sum once;
+// adding in FP32 first changes nothing (a sum of two bf16 values that FP32
+// cannot hold is further from a bf16 tie than FP32's rounding).
+struct BfChunk {
+  uint4 v;
+};
+struct F32Chunk {
+  float4 a, b;
+};
+__device__ __forceinline__ void stream_sum(const __nv_bfloat16 *x, const __nv_bfloat16 *r, float (&f)[8], BfChunk &c) {
+  c.v = *reinterpret_cast<const uint4 *>(x);
+  uint32_t w[4] = {c.v.x, c.v.y, c.v.z, c.v.w};
+  if (r) {
+    const uint4 g = *reinterpret_cast<const uint4 *>(r);
+    const uint32_t u[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 t = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]),
+                                          *reinterpret_cast<const __nv_bfloat162 *>(&u[i]));
+      w[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    c.v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <bool SHARED>
+__device__ __forceinline__ void stream_sum_f32(const float *x, const float *r, float (&f)[8]) {
+  if (SHARED)
+    load8_sh(x, f);
+  else
+    load8(x, f);
+  if (r) {
+    float g[8];
+    if (SHARED)
+      load8_sh(r, g);
+    else
+      load8(r, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += g[i];
+  }
+}
+__device__ __forceinline__ void store_h(__nv_bfloat16 *p, const float (&)[8], const BfChunk &c) {
+  *reinterpret_cast<uint4 *>(p) = c.v;
+}
+__device__ __forceinline__ void store_h(float *p, const float (&f)[8], const F32Chunk &) { store8(p, f); }
+template <bool SHARED>
+__device__ __forceinline__ void load_h(const __nv_bfloat16 *x, const __nv_bfloat16 *r, float (&f)[8], BfChunk &c) {
+  stream_sum(x, r, f, c);
+}
+template <bool SHARED>
+__device__ __forceinline__ void load_h(const float *x, const float *r, float (&f)[8], F32Chunk &) {
+  stream_sum_f32<SHARED>(x, r, f);
+}
+template <typename TS>
+struct ChunkOf {
+  using type = F32Chunk;
+};
+template <>
+struct ChunkOf<__nv_bfloat16> {
+  using type = BfChunk;
+};
+
+__device__ __forceinline__ float sum_sq(const float (&f)[8], float ss) {
+  float o = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) ffma2_vec(ss, o, f[i], f[i + 1], f[i], f[i + 1]);
+  return ss + o;
+}
 
 // Sum over the threads of one row (threadIdx.x; blockDim.x a multiple of 32):
 // a butterfly in each warp, then the warps' sums in warp order.  Every thread
@@ -91,15 +175,18 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
 }
 
 // Codes of 8 values of a tile with scale S.  y carries FP32 rounding already,
-// so y times the reciprocal of S (2 roundings) serves for the quotient; a tiny
-// S, whose reciprocal overflows, takes the division, and a NaN one gives NaN
-// codes.
-__device__ __forceinline__ uint2 tile_codes(const float (&f)[8], float S) {
+// so y times the reciprocal of S (one Newton step on the hardware's: 2
+// roundings in all) serves for the quotient; a tiny S, whose reciprocal
+// overflows, takes the division, and a NaN one gives NaN codes.
+__device__ __forceinline__ uint2 tile_codes(float (&f)[8], float S) {
   uint32_t lo = 0, hi = 0;
   if (S >= 0x1p-100f) {
-    const float r = __frcp_rn(S);
-    lo = e4m3x2_rn_sat(f[0] * r, f[1] * r) | (e4m3x2_rn_sat(f[2] * r, f[3] * r) << 16);
-    hi = e4m3x2_rn_sat(f[4] * r, f[5] * r) | (e4m3x2_rn_sat(f[6] * r, f[7] * r) << 16);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(S));
+    r = fmaf(fmaf(-S, r, 1.0f), r, r);
+    mul8(f, r);
+    lo = e4m3x2_rn_sat(f[0], f[1]) | (e4m3x2_rn_sat(f[2], f[3]) << 16);
+    hi = e4m3x2_rn_sat(f[4], f[5]) | (e4m3x2_rn_sat(f[6], f[7]) << 16);
   } else if (S != 0.0f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) lo |= static_cast<uint32_t>(e4m3_rn_sat(f[i] / S)) << (8 * i);
@@ -109,10 +196,15 @@ __device__ __forceinline__ uint2 tile_codes(const float (&f)[8], float S) {
   return make_uint2(lo, hi);
 }
 
-// max(|a|, |b|), NaN if either is
+// max(|a|, |b|) and max(|a|, |b|, |c|), NaN if one is
 __device__ __forceinline__ float amax_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float amax_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -123,7 +215,30 @@ __device__ __forceinline__ float tile_scale(float am) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) am = amax_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
   if (!(am <= 3.402823466e38f)) return __uint_as_float(0x7FFFFFFFu);
-  return POW2 ? pow2_scale(am) : am / 448.0f;
+  if (POW2) return pow2_scale(am);
+  // am / 448, correctly rounded: through 1 / 448 and one residual, by the
+  // division where that could leave the normal range
+  return am >= 0x1p-100f ? div_by_recip(am, 448.0f, 1.0f / 448.0f) : am / 448.0f;
+}
+
+// What is left of a chunk once rstd is known: y (stored as bf16 if y is given),
+// the tile's scale, the codes.  Every lane of the warp calls it; `in`: the chunk
+// is inside the row (a tile's 16 lanes all are, or none).  f: h, overwritten.
+template <bool POW2>
+__device__ __forceinline__ void finish_chunk(float (&f)[8], const float (&w)[8], float rstd, bool in,
+                                             __nv_bfloat16 *y, uint8_t *q, float *s) {
+  mul8(f, rstd);
+  mul8(f, w);
+  float am = 0.0f;
+  if (in) {
+    am = amax_nan(amax_nan(f[0], f[1], f[2]), amax_nan(f[3], f[4], f[5]), amax_nan(f[6], f[7]));
+    if (y) store8(y, f);
+  }
+  const float S = tile_scale<POW2>(am);
+  if (in) {
+    *reinterpret_cast<uint2 *>(q) = tile_codes(f, S);
+    if ((threadIdx.x & 15) == 0) *s = S;
+  }
 }
 
 struct NormFwd {
@@ -152,6 +267,7 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
   const bool live = r < p.rows;
   const int nch = p.cols / 8;
   float f[CH][8];
+  typename ChunkOf<TS>::type hc[CH];
   float ss = 0.0f;
   const TS *x = static_cast<const TS *>(p.x) + r * p.ld_x;
   const TS *rs = p.resid ? static_cast<const TS *>(p.resid) + r * p.ld_r : nullptr;
@@ -160,18 +276,8 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
     const int c = threadIdx.x + k * blockDim.x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[k][i] = 0.0f;
-    if (live && c < nch) {
-      load8(x + c * 8, f[k]);
-      if (rs) {
-        float g[8];
-        load8(rs + c * 8, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[k][i] += g[i];
-        round8(x, f[k]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(f[k][i], f[k][i], ss);
-    }
+    if (live && c < nch) load_h<false>(x + c * 8, rs ? rs + c * 8 : nullptr, f[k], hc[k]);
+    ss = sum_sq(f[k], ss);
   }
   ss = row_sum(ss, buf);
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
@@ -179,27 +285,16 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = threadIdx.x + k * blockDim.x;
-    // a tile's 16 lanes are all inside or all outside the row
     const bool in = live && c < nch;
-    if (in && p.h) store8(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k]);
-    float am = 0.0f;
-    if (in) {
-      float w[8];
+    float w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (in) {
+      if (p.h) store_h(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k], hc[k]);
       if (p.w) load8(p.w + c * 8, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[k][i] = f[k][i] * rstd * w[i];
-        am = amax_nan(am, f[k][i]);
-      }
-      if (p.y) store8(p.y + r * p.cols + c * 8, f[k]);
     }
-    const float S = tile_scale<POW2>(am);
-    if (in) {
-      *reinterpret_cast<uint2 *>(p.q + r * p.cols + c * 8) = tile_codes(f[k], S);
-      if ((threadIdx.x & 15) == 0) p.s[r * (p.cols / 128) + (c >> 4)] = S;
-    }
+    finish_chunk<POW2>(f[k], w, rstd, in, p.y ? p.y + r * p.cols + c * 8 : nullptr, p.q + r * p.cols + c * 8,
+                       p.s + r * (p.cols / 128) + (c >> 4));
   }
 }
 
@@ -363,23 +458,14 @@ __global__ void __launch_bounds__(MAXT, MINB) add_rmsnorm_quant_ring_kernel(cons
     const bool ok = mbar_wait(&bars.full[s], (it / stages) & 1, ctl);
     const TS *x = reinterpret_cast<const TS *>(ring + s * stage_bytes);
     float f[2][8], ss = 0.0f;
+    typename ChunkOf<TS>::type hc[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[k][i] = 0.0f;
-      if (c < nch) {
-        load8_sh(x + c * 8, f[k]);
-        if (p.resid) {
-          float g[8];
-          load8_sh(x + p.cols + c * 8, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[k][i] += g[i];
-          round8(x, f[k]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[k][i], f[k][i], ss);
-      }
+      if (c < nch) load_h<true>(x + c * 8, p.resid ? x + p.cols + c * 8 : nullptr, f[k], hc[k]);
+      ss = sum_sq(f[k], ss);
     }
     ss = ring_sum(ss, bars.red[it & 1]);
     if (threadIdx.x == 0) copy_in(it + stages);
@@ -390,19 +476,9 @@ __global__ void __launch_bounds__(MAXT, MINB) add_rmsnorm_quant_ring_kernel(cons
     for (int k = 0; k < 2; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
       const bool in = c < nch;
-      if (in && p.h) store8(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k]);
-      float am = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[k][i] = f[k][i] * rstd * w[k][i];
-        if (in) am = amax_nan(am, f[k][i]);
-      }
-      if (in && p.y) store8(p.y + r * p.cols + c * 8, f[k]);
-      const float S = tile_scale<POW2>(am);
-      if (in) {
-        *reinterpret_cast<uint2 *>(p.q + r * p.cols + c * 8) = tile_codes(f[k], S);
-        if ((threadIdx.x & 15) == 0) p.s[r * (p.cols / 128) + (c >> 4)] = S;
-      }
+      if (in && p.h) store_h(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k], hc[k]);
+      finish_chunk<POW2>(f[k], w[k], rstd, in, p.y ? p.y + r * p.cols + c * 8 : nullptr, p.q + r * p.cols + c * 8,
+                         p.s + r * (p.cols / 128) + (c >> 4));
     }
   }
   ring_drain(&bars, stages, it);

@@ -548,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
 // SM has the same work.  The tensor core's FP32 accumulation drops the bits
 // below its 24 at every step (measured: the error grows with the number of
 // steps, to 6e-6 of the result over 3300 tokens), so one TMEM accumulator takes
-// WR_CHUNK stages (48 steps) at most: the epilogue warps add it into FP32
+// WR_CHUNK stages (24 steps) at most: the epilogue warps add it into FP32
 // registers while the next chunk's MMAs fill the other buffer.  At the end of a
 // strip's run the registers go to the partial sums, piece (pair + strip).
 // A stage is two loads, one 4D box of the parts and one 3D box of x: as eight
@@ -557,7 +557,7 @@ namespace {
 constexpr int WR_THREADS = 384;              // warp 0 TMA, warp 1 MMA (even CTA), warps 4..11 epilogue
 constexpr int WR_STAGES = 3;
 constexpr int WR_TOK = 64;                   // tokens (K) per stage
-constexpr int WR_CHUNK = 4;                  // stages per TMEM accumulation
+constexpr int WR_CHUNK = 2;                  // stages per TMEM accumulation
 constexpr int WR_G = WR_TOK * 128;           // 64 tokens x 64 experts (or columns)
 constexpr int WR_A = kParts * 2 * WR_G;      // this CTA's 128 experts
 constexpr int WR_B = 2 * WR_G;               // this CTA's 128 columns
