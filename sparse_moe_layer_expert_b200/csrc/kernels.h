@@ -268,8 +268,9 @@ size_t router_dwr_scratch(int64_t T, int cols);  // bytes of launch_router_dwr's
 cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st);
 cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
                              int32_t *err, uint64_t limit_ns, cudaStream_t st);
+// behind_dx: launch_router_dx came directly before it on the stream (else launch_router_dz)
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
-                              int32_t *err, uint64_t limit_ns, cudaStream_t st);
+                              bool behind_dx, int32_t *err, uint64_t limit_ns, cudaStream_t st);
 
 // weight-block pairs (tiles) per chunk of activations in each grouped GEMM
 __host__ __device__ inline int gemm1_blocks(int I) { return I / 128; }

@@ -20,12 +20,14 @@
 //   router_dz_kernel   a warp per run of tokens: dz, written in FP32 (when asked
 //                      for) and as parts [3][T][Np] bf16, Np = N_r rounded up
 //                      to 64 (zeros behind N_r)
-//   router_dx_kernel   persistent over 128-token tiles of one 256-column strip
-//                      of W_r, which stays in shared memory (K = Np <= 256);
-//                      A = the parts (K-major), B = W_r as it lies (N-major)
-//   router_dwr_kernel  all experts x 256 columns of x per CTA over a range of
-//                      tokens, so x is read once; both operands M/N-major
-//                      (tokens are the slow index of both)
+//   router_dx_kernel   256 tokens x 256 columns per pair of CTAs, a token tile's
+//                      parts resident over its strips of W_r; A = the parts
+//                      (K-major), B = W_r as it lies (N-major)
+//   router_dwr_kernel  all experts x 256 columns of x per pair of CTAs over a
+//                      range of tokens, so x is read once; both operands
+//                      M/N-major (tokens are the slow index of both).  It needs
+//                      dz alone and starts on the SMs that router_dx_kernel
+//                      leaves
 //   dwr_join_kernel    adds the token ranges' partial sums in range order
 #include "common.cuh"
 #include "kernels.h"
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(256, B == 1 ? 4 : 2) router_dz_kernel(const Dz
       float z[EPL];
       load_logits<VEC, B>(a.partial, a.n_ks, a.T, a.Nr, t, lane, z);
       if (t >= seq_end) {
-        const int s = seq_of(a.off, a.n_seq, t);
+        const int s = seq_of(a.off, a.n_seq, t, lane);
         seq = -1;
         seq_end = a.T;
         if (s < a.n_seq) {
@@ -397,8 +399,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
   const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, args.n_strips * args.m_tiles);
   const int nk = args.kb * X_KPB;  // stages per unit
-  dependents_start();
+  // in this order: what starts behind this kernel (router_dwr_kernel) relies on
+  // dz being complete by then
   predecessor_done();
+  dependents_start();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -577,6 +581,7 @@ struct DwrArgs {
   int n_strips, n_stages;  // H / 256 and T / 64, rounded up
   int Nr;
   float *part;             // [pairs + n_strips, 256, 256]
+  int behind_dx;           // launched behind router_dx_kernel, not router_dz_kernel
   int32_t *err;
   uint64_t limit_ns;
 };
@@ -629,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   const PairUnits pu = pair_units(pair, gridDim.x >> 1, args.n_strips * args.n_stages);
 
   dependents_start();
-  predecessor_done();
+  if (!args.behind_dx) predecessor_done();
 
   // Register split as in gemm_pair.cu: 128 * 72 + 256 * 216 = 384 * 168
   if (warp < 4) {
@@ -700,16 +705,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
     setmaxnreg_inc<216>();
     const int q = warp & 3;
     const int wg = (warp - 4) >> 2;
-    const int row = rank * 128 + q * 32 + lane;          // expert
     const bool live = rank * 128 + q * 32 < args.Nr;     // any expert in this warp
     uint32_t tc = 0;
     bool stop = false;
     for (int u = pu.u0; u < pu.u1 && !stop;) {
       const int strip = u / args.n_stages;
       const int end = run_end(u, pu.u1, args.n_stages);
-      float acc[128];
+      // 16-row halves h, 32-column blocks c: lane 4 i + j holds rows i, i + 8 and
+      // columns 2 j, 2 j + 1 of each 8-column block (tmem_ld_16x256)
+      float acc[2][4][16];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
       for (; u < end; u += WR_CHUNK, ++tc) {
         const uint32_t buf = tc & 1;
         if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) {
@@ -720,22 +730,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
           tc_fence_after();
           const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[64];
-            tmem_ld64(ta + c * 64, v);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[2][16];
+            tmem_ld_16x256(ta + c * 32, v[0]);
+            tmem_ld_16x256(ta + c * 32 + (1 << 20), v[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[c * 64 + j] += __uint_as_float(v[j]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[h][c][j] += __uint_as_float(v[h][j]);
           }
           tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
       }
-      if (row < args.Nr) {
-        float *o = args.part + (static_cast<int64_t>(pair + strip) * 256 + row) * 256 + wg * 128;
+      if (live) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 8) st_f32x8(o + j, acc + j);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r8 = 0; r8 < 2; ++r8) {
+            const int row = rank * 128 + q * 32 + h * 16 + r8 * 8 + (lane >> 2);  // expert
+            float *o = args.part + (static_cast<int64_t>(pair + strip) * 256 + row) * 256 + wg * 128 + (lane & 3) * 8;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float f[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                f[2 * j] = acc[h][c][4 * j + 2 * r8];
+                f[2 * j + 1] = acc[h][c][4 * j + 2 * r8 + 1];
+              }
+              quad_transpose(f, lane);
+              if (row < args.Nr) st_f32x8(o + c * 32, f);
+            }
+          }
       }
       u = end;
     }
@@ -744,6 +772,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  // what follows this kernel on the stream comes behind router_dx_kernel too
+  if (args.behind_dx) predecessor_done();
 }
 
 // dW_r [Nr, cols] from the pieces of each strip, in token order.  CTA (4
@@ -827,7 +857,7 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
   a.parts = static_cast<__nv_bfloat16 *>(g.parts);
   a.Np = router_parts_pitch(g.Nr);
   a.err = g.err;
-  // four warps per scheduler at once, and no more tokens per warp than that takes
+  // as many warps as are resident at once (four CTAs on every SM)
   const int64_t warps = static_cast<int64_t>(moe_host::sm_count()) * 32;
   const int64_t run = (g.T + warps - 1) / warps;
   a.run = static_cast<int>(run < 8 ? run : 8);
@@ -871,7 +901,7 @@ cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int N
 }
 
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
-                              int32_t *err, uint64_t limit_ns, cudaStream_t st) {
+                              bool behind_dx, int32_t *err, uint64_t limit_ns, cudaStream_t st) {
   if (T == 0) return cudaMemsetAsync(dwr, 0, sizeof(float) * Nr * static_cast<size_t>(H), st);
   const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
   DwrArgs a{};
@@ -880,6 +910,7 @@ cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int N
   a.n_stages = dwr_stages(T);
   a.Nr = Nr;
   a.part = part;
+  a.behind_dx = behind_dx;
   a.err = err;
   a.limit_ns = limit_ns;
   // both operands in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], x [H / 64][T][64]

@@ -104,7 +104,7 @@ __device__ __forceinline__ float load_logit(const float *__restrict__ partial, i
 // hardware's (1 ulp), as these feed gradients and sums, not the selection.
 __device__ __forceinline__ void sigmoid_pair(float z, float &s, float &om) {
   const float q = expf(-z);
-  s = __fdividef(1.0f, 1.0f + q);  // q = inf gives 0
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + q));  // q = inf gives 0
   om = z >= 0.0f ? q * s : 1.0f - s;
 }
 
@@ -115,16 +115,21 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The first sequence that ends behind token t (n_seq if none does): sequence
-// s holds the tokens [off[s], off[s + 1]).  Offsets come from device memory
-// and may be wrong: whatever they hold, the result is in [0, n_seq].
-__device__ __forceinline__ int seq_of(const int32_t *__restrict__ off, int n_seq, int64_t t) {
-  int lo = 0, hi = n_seq;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid + 1] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+// s holds the tokens [off[s], off[s + 1]).  A warp searches together, 32 probes
+// a step.  Offsets come from device memory and may be wrong: whatever they
+// hold, the result is in [0, n_seq], and its end is behind t if it is below
+// n_seq.
+__device__ __forceinline__ int seq_of(const int32_t *__restrict__ off, int n_seq, int64_t t, int lane) {
+  int lo = 0, n = n_seq;  // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int last = (lane + 1) * step - 1;  // of this lane's group of sequences
+    const bool before = last < n && off[lo + last + 1] <= t;
+    const uint32_t not_before = ~__ballot_sync(0xffffffffu, before);
+    const int c = not_before ? __ffs(not_before) - 1 : 32;  // groups that end at or before t
+    const bool whole = (c + 1) * step <= n;                  // group c's last sequence was probed: it ends behind t
+    lo += c * step;
+    n = whole ? step - 1 : n - c * step;
   }
   return lo;
 }
