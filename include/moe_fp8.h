@@ -605,7 +605,9 @@ typedef struct {
  *   dwr_dev     float [N_r, H], nullable (T == 0 writes zeros)
  *   ws_dev      moe_router_backward_workspace_size() bytes, 256-byte aligned
  *               (only with dx_dev or dwr_dev)
- *   err_flag_dev as in moe_balance_loss */
+ *   err_flag_dev gets MOE_DEVERR_BAD_INDEX for an expert index out of range
+ *               (its slot is left out); the offsets' check is
+ *               moe_balance_loss's */
 MOE_API size_t moe_router_backward_workspace_size(const moe_config *cfg, int64_t T);
 MOE_API int moe_router_backward(const moe_config *cfg, const float *logits_dev, int32_t n_splits,
                                 const int32_t *idx_dev, int64_t T, const float *dgate_dev,

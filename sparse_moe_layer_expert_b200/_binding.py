@@ -471,13 +471,21 @@ def _cuda_index(where: str, t, name: str) -> int:
     return idx
 
 
-def _on_device(fn, idx: int, stream, where: str, args) -> None:
+def _use_stream(stream, t):
+    """Context: `stream` (a torch stream or a handle) as the current one, so
+    that what a call allocates (workspaces, outputs) belongs to the stream it
+    runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        dev = getattr(t, "device", None)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def _on_device(fn, idx: int, where: str, args) -> None:
     """fn(*args, stream) with device `idx` current (the library launches on
-    the current device), on the caller's stream or that device's current one."""
-    if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(idx)
-    else:
-        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    the current device), on that device's current stream."""
+    st = torch._C._cuda_getCurrentRawStream(idx)
     if idx == torch._C._cuda_getDevice():
         status = fn(*args, st)
     else:
@@ -503,6 +511,9 @@ def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: f
     pass.  x, resid: bf16 or float32 [rows, cols] (rows may be strided);
     weight: float32 [cols] or None.  Returns (h, y bf16, q uint8, scales,
     rstd); without resid, h is x unless a buffer is given."""
+    if stream is not None:
+        with _use_stream(stream, x):
+            return fp8_add_rmsnorm_quant_1x128(x, resid, weight, eps, h, y, q, scales, rstd, pow2)
     where = "fp8_add_rmsnorm_quant_1x128"
     code, idx = _stream_type(where, x, "x"), _cuda_index(where, x, "x")
     shape = x.shape
@@ -532,7 +543,7 @@ def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: f
         scales = torch.empty((rows, cols // 128), dtype=_F32, device=dev)
     if rstd is None:
         rstd = torch.empty((rows,), dtype=_F32, device=dev)
-    _on_device(lib.fp8_add_rmsnorm_quant_1x128, idx, stream, where, (
+    _on_device(lib.fp8_add_rmsnorm_quant_1x128, idx, where, (
         x.data_ptr(), ld, rp, ldr, code, None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
         eps, rows, cols, None if h is None else _want(where, h, "h", dtype, shape, idx),
         _want(where, y, "y", _BF16, shape, idx), _want(where, q, "q", _U8, shape, idx),
@@ -546,6 +557,9 @@ def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, 
     quantization): (dx, dweight).  dy: gradient of y (bf16 or float32); h,
     rstd: the forward's; dres: gradient reaching h past the norm, of h's type.
     dx (the gradient of x and of resid) has dx_dtype, by default h's type."""
+    if stream is not None:
+        with _use_stream(stream, h):
+            return add_rmsnorm_backward(dy, h, rstd, weight, dres, dx, dw, dx_dtype, ws)
     where = "add_rmsnorm_backward"
     code, idx = _stream_type(where, h, "h"), _cuda_index(where, h, "h")
     shape, dtype = h.shape, h.dtype
@@ -562,7 +576,7 @@ def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, 
         dw = torch.empty((cols,), dtype=_F32, device=h.device)
     if ws is None:
         ws = _scratch(lib.add_rmsnorm_backward_workspace_size, idx, rows, cols)
-    _on_device(lib.add_rmsnorm_backward, idx, stream, where, (
+    _on_device(lib.add_rmsnorm_backward, idx, where, (
         _want(where, dy, "dy", dy.dtype, shape, idx), ycode, _want(where, h, "h", dtype, shape, idx),
         None if dres is None else _want(where, dres, "dres", dtype, shape, idx), code,
         None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
@@ -611,6 +625,9 @@ def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e
     (loss [n_seq], counts int32 [n_seq, N_r]).  logits: float32 [n_splits, T,
     N_r] (moe_route_logits, or the caller's own with n_splits = 1); idx: the
     picks; seq_offsets: int32 [n_seq + 1]."""
+    if stream is not None:
+        with _use_stream(stream, logits):
+            return moe_balance_loss(cfg, logits, idx, seq_offsets, alpha, loss, counts, ws, err)
     where = "moe_balance_loss"
     n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
     n_seq, op = _sequences(where, seq_offsets, dev)
@@ -623,7 +640,7 @@ def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e
         ws = _scratch(lib.moe_balance_loss_workspace_size, dev, cp, T, n_seq)
     if err is None:
         err = new_err_flag(logits.device)
-    _on_device(lib.moe_balance_loss, dev, stream, where, (
+    _on_device(lib.moe_balance_loss, dev, where, (
         cp, zp, n, ip, T, op, n_seq, alpha, _want(where, loss, "loss", _F32, (n_seq,), dev),
         _want(where, counts, "counts", _I32, (n_seq, cfg.n_routed), dev), _want(where, ws, "ws", _U8, None, dev),
         ws.numel(), _want(where, err, "err", _I32, None, dev)))
@@ -646,6 +663,9 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
     dgate: gradient of the gates, float32 [T, K_r]; balance: dict(seq_offsets,
     counts, dloss (None: ones), alpha) of the balance loss; x bf16 [T, H] for
     dwr, wr bf16 [N_r, H] for dx.  dx_accumulate adds to dx."""
+    if stream is not None:
+        with _use_stream(stream, logits):
+            return moe_router_backward(cfg, logits, idx, x, wr, dgate, balance, dlogits, dx, dx_accumulate, dwr, ws, err)
     where = "moe_router_backward"
     n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
     H, Nr = cfg.hidden, cfg.n_routed
@@ -667,7 +687,7 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
         ws = _scratch(lib.moe_router_backward_workspace_size, dev, cp, T)
     if err is None:
         err = new_err_flag(logits.device)
-    _on_device(lib.moe_router_backward, dev, stream, where, (
+    _on_device(lib.moe_router_backward, dev, where, (
         cp, zp, n, ip, T, None if dgate is None else _want(where, dgate, "dgate", _F32, (T, cfg.top_k), dev),
         None if balance is None else C.byref(_balance_struct(where, cfg, balance, dev)),
         None if x is None and dwr is None else _want(where, x, "x", _BF16, (T, H), dev),
@@ -683,6 +703,10 @@ def moe_block_forward(cfg: MoeConfig, w: dict, bias, x, resid=None, norm_weight=
     """The layer with the norm in front: h = x + resid, out = h + MoE(norm(h)).
     Returns (out, h, y, rstd); the last three and the workspace are what
     moe_block_backward reads.  w as moe_forward's."""
+    if stream is not None:
+        with _use_stream(stream, x):
+            return moe_block_forward(cfg, w, bias, x, resid, norm_weight, eps, h, y, rstd, out, out_dtype, idx_out, counts_out,
+                                     ws, err)
     where = "moe_block_forward"
     idx = _cuda_index(where, x, "x")
     if x.dim() != 2 or x.shape[1] != cfg.hidden:
@@ -697,7 +721,7 @@ def moe_block_forward(cfg: MoeConfig, w: dict, bias, x, resid=None, norm_weight=
     ws = _scratch(lib.moe_workspace_size, idx, cp, T) if ws is None else ws
     err = new_err_flag(dev) if err is None else err
     wst = weights_struct(w)
-    _on_device(lib.moe_block_forward, idx, stream, where, (
+    _on_device(lib.moe_block_forward, idx, where, (
         cp, C.byref(wst), _want(where, bias, "bias", _F32, (cfg.n_routed,), idx),
         None if norm_weight is None else _want(where, norm_weight, "norm_weight", _F32, (H,), idx), eps,
         _want(where, x, "x", _BF16, shape, idx),
@@ -716,6 +740,10 @@ def moe_block_backward(cfg: MoeConfig, w: dict, wt: dict, h, y, rstd, dout, fwd_
     """Every gradient of moe_block_forward for the batch whose forward left
     its state in fwd_ws: (dx [T, H] bf16 (or dx_dtype), dnorm [H], dwr [N_r,
     H], dW13 [E, 2I, H], dW2 [E, H, I]).  balance: as moe_router_backward's."""
+    if stream is not None:
+        with _use_stream(stream, h):
+            return moe_block_backward(cfg, w, wt, h, y, rstd, dout, fwd_ws, norm_weight, balance, dx, dnorm, dwr, dW13, dW2,
+                                      dx_dtype, ws, err)
     where = "moe_block_backward"
     idx = _cuda_index(where, h, "h")
     if h.dim() != 2 or h.shape[1] != cfg.hidden:
@@ -734,7 +762,7 @@ def moe_block_backward(cfg: MoeConfig, w: dict, wt: dict, h, y, rstd, dout, fwd_
     ws = _scratch(lib.moe_block_backward_workspace_size, idx, cp, T) if ws is None else ws
     err = new_err_flag(dev) if err is None else err
     wst = weights_struct(w)
-    _on_device(lib.moe_block_backward, idx, stream, where, (
+    _on_device(lib.moe_block_backward, idx, where, (
         cp, C.byref(wst), _ptr(wt["w13t"]), _ptr(wt["s13t"]), _ptr(wt["w2t"]), _ptr(wt["s2t"]),
         None if norm_weight is None else _want(where, norm_weight, "norm_weight", _F32, (H,), idx),
         _want(where, h, "h", _BF16, shape, idx), _want(where, y, "y", _BF16, shape, idx),

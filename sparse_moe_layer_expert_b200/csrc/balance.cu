@@ -119,10 +119,11 @@ __global__ void __cluster_dims__(BAL_CTAS, 1, 1) __launch_bounds__(BAL_JW * 32)
   __shared__ float p_sh[BAL_JW][32];
   __shared__ int c_sh[BAL_JW][32];
   __shared__ float term;
-  const int s = blockIdx.y, rank = static_cast<int>(cluster_ctarank());
+  const int s = blockIdx.x / BAL_CTAS, rank = static_cast<int>(cluster_ctarank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = rank * 32 + (lane & 7) * 4;
   const int sl = warp * 4 + (lane >> 3);  // 64 slices
+  predecessor_done();
   int64_t b0 = a.off[s], b1 = a.off[s + 1];
   if (b0 < 0 || b1 < b0 || b1 > a.T) {  // wrong offsets: reported, and read as an empty sequence
     if (rank == 0 && threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_BAD_INDEX);
@@ -130,7 +131,6 @@ __global__ void __cluster_dims__(BAL_CTAS, 1, 1) __launch_bounds__(BAL_JW * 32)
   }
   float p[4] = {0.f, 0.f, 0.f, 0.f};
   int c[4] = {0, 0, 0, 0};
-  predecessor_done();
   if (e0 < a.Nr && b1 > b0) {
     const int k0 = static_cast<int>(b0 / a.chunk), k1 = static_cast<int>((b1 - 1) / a.chunk);
     if (a.Nr % 4 == 0) {
@@ -232,7 +232,7 @@ cudaError_t launch_balance_loss(const float *partial, int n_ks, int64_t T, int N
     kernel<<<a.n_chunks, BAL_WARPS * 32, 0, st>>>(a);
   }
   if (const cudaError_t e = cudaGetLastError()) return e;
-  return launch_next(balance_join_kernel, dim3(BAL_CTAS, n_seq), dim3(BAL_JW * 32), 0, st, a, alpha, loss, counts);
+  return launch_next(balance_join_kernel, dim3(static_cast<unsigned>(BAL_CTAS) * n_seq), dim3(BAL_JW * 32), 0, st, a, alpha, loss, counts);
 }
 
 }  // namespace moe

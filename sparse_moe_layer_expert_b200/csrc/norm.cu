@@ -384,25 +384,33 @@ struct RingBars {
   int abort_flag;
 };
 
-// Sum over the CTA: each warp's sum into `red`, one barrier, the warps' sums in
-// a fixed order.  red[nwarps..31] stay zero.
+// This thread of the CTA, over both dimensions.
+__device__ __forceinline__ int tid() { return threadIdx.y * blockDim.x + threadIdx.x; }
+
+// Sum over the threads of one row (threadIdx.x): each warp's sum into `red`, one
+// barrier of the CTA, the row's warps' sums in a fixed order.  red's slots
+// behind the CTA's warps stay zero.
 __device__ __forceinline__ float ring_sum(float v, float *red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[tid() >> 5] = v;
   __syncthreads();
+  const int nw = blockDim.x >> 5;
   float s = 0.0f;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); i += 4) {
-    const float4 q = *reinterpret_cast<const float4 *>(red + i);
-    s += (q.x + q.y) + (q.z + q.w);
+  if (blockDim.y == 1) {
+    for (int i = 0; i < nw; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(red + i);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+  } else {
+    for (int i = 0; i < nw; ++i) s += red[threadIdx.y * nw + i];
   }
   return s;
 }
 
 __device__ __forceinline__ void ring_init(RingBars *b, int stages) {
-  if (threadIdx.x < 64) b->red[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
-  if (blockDim.x < 64 && threadIdx.x < 32) b->red[1][threadIdx.x] = 0.0f;
-  if (threadIdx.x == 0) {
+  for (int i = tid(); i < 64; i += blockDim.x * blockDim.y) b->red[i >> 5][i & 31] = 0.0f;
+  if (tid() == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&b->full[i], 1);
     b->abort_flag = 0;
     fence_mbar_init();
@@ -413,7 +421,7 @@ __device__ __forceinline__ void ring_init(RingBars *b, int stages) {
 // Copies still in flight (only after a wait that gave up) land before the CTA
 // leaves.
 __device__ __forceinline__ void ring_drain(RingBars *b, int stages, uint32_t rows) {
-  if (threadIdx.x == 0 && b->abort_flag) {
+  if (tid() == 0 && b->abort_flag) {
     int quiet = 0;
     const WaitCtl drain{&quiet, nullptr, 100000000ull};
     const uint32_t n = rows < static_cast<uint32_t>(stages) ? rows : stages;
@@ -484,27 +492,31 @@ __global__ void __launch_bounds__(MAXT, MINB) add_rmsnorm_quant_ring_kernel(cons
   ring_drain(&bars, stages, it);
 }
 
+// Backward.  blockDim = (threads per row, rows per stage): short rows go several
+// to a stage (they are contiguous), each with its own warps.
 template <typename TY, typename TS, typename TX, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int stages) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) RingBars bars;
   dependents_start();
-  const int nch = p.cols / 8;
+  const int nch = p.cols / 8, nrow = blockDim.y, ty = threadIdx.y;
   const uint32_t y_bytes = static_cast<uint32_t>(p.cols * sizeof(TY)), s_bytes = static_cast<uint32_t>(p.cols * sizeof(TS));
-  const uint32_t stage_bytes = y_bytes + (p.dres ? 2 * s_bytes : s_bytes);
+  const uint32_t row_bytes = y_bytes + (p.dres ? 2 * s_bytes : s_bytes);
+  const uint32_t h_off = nrow * y_bytes, d_off = h_off + nrow * s_bytes, stage_bytes = nrow * row_bytes;
   ring_init(&bars, stages);
-  const int64_t step = gridDim.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * nrow, first = static_cast<int64_t>(blockIdx.x) * nrow;
   auto copy_in = [&](uint32_t i) {
-    const int64_t r = blockIdx.x + i * step;
+    const int64_t r = first + i * step;
     if (r >= p.rows) return;
+    const uint32_t n = p.rows - r < nrow ? static_cast<uint32_t>(p.rows - r) : nrow;
     uint8_t *st = ring + (i % stages) * stage_bytes;
     uint64_t *bar = &bars.full[i % stages];
-    mbar_arrive_expect_tx(bar, stage_bytes);
-    bulk_load(st, static_cast<const TY *>(p.dy) + r * p.cols, y_bytes, bar);
-    bulk_load(st + y_bytes, static_cast<const TS *>(p.h) + r * p.cols, s_bytes, bar);
-    if (p.dres) bulk_load(st + y_bytes + s_bytes, static_cast<const TS *>(p.dres) + r * p.cols, s_bytes, bar);
+    mbar_arrive_expect_tx(bar, n * row_bytes);
+    bulk_load(st, static_cast<const TY *>(p.dy) + r * p.cols, n * y_bytes, bar);
+    bulk_load(st + h_off, static_cast<const TS *>(p.h) + r * p.cols, n * s_bytes, bar);
+    if (p.dres) bulk_load(st + d_off, static_cast<const TS *>(p.dres) + r * p.cols, n * s_bytes, bar);
   };
-  if (threadIdx.x == 0)
+  if (tid() == 0)
     for (int i = 0; i < stages; ++i) copy_in(i);
   float w[2][8], dw[2][8];
 #pragma unroll
@@ -519,8 +531,10 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const Nor
   }
   const WaitCtl ctl{&bars.abort_flag, nullptr, kDefaultWaitLimitNs};
   uint32_t it = 0;
-  float next = blockIdx.x < p.rows ? __ldg(p.rstd + blockIdx.x) : 0.0f;
-  for (int64_t r = blockIdx.x; r < p.rows; r += step, ++it) {
+  float next = first + ty < p.rows ? __ldg(p.rstd + first + ty) : 0.0f;
+  for (int64_t r0 = first; r0 < p.rows; r0 += step, ++it) {
+    const int64_t r = r0 + ty;
+    const bool live = r < p.rows;
     float rstd = next;
     if (r + step < p.rows) next = __ldg(p.rstd + r + step);
     const int s = it % stages;
@@ -531,12 +545,12 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const Nor
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
-      if (c < nch) {
-        load8_sh(reinterpret_cast<const TY *>(st) + c * 8, g[k]);
-        load8_sh(reinterpret_cast<const TS *>(st + y_bytes) + c * 8, n[k]);
+      if (live && c < nch) {
+        load8_sh(reinterpret_cast<const TY *>(st + ty * y_bytes) + c * 8, g[k]);
+        load8_sh(reinterpret_cast<const TS *>(st + h_off + ty * s_bytes) + c * 8, n[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[k][i] = 0.0f;
-        if (p.dres) load8_sh(reinterpret_cast<const TS *>(st + y_bytes + s_bytes) + c * 8, d[k]);
+        if (p.dres) load8_sh(reinterpret_cast<const TS *>(st + d_off + ty * s_bytes) + c * 8, d[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           n[k][i] *= rstd;
@@ -547,25 +561,47 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const Nor
       }
     }
     const float m = ring_sum(sum, bars.red[it & 1]) / static_cast<float>(p.cols);
-    if (threadIdx.x == 0) copy_in(it + stages);
+    if (tid() == 0) copy_in(it + stages);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
-      if (c < nch) {
+      if (live && c < nch) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[k][i] = fmaf(rstd, fmaf(-n[k][i], m, g[k][i]), d[k][i]);
         store8(static_cast<TX *>(p.dx) + r * p.cols + c * 8, d[k]);
       }
     }
   }
-  if (p.dw_part) {
+  ring_drain(&bars, stages, it);
+  if (!p.dw_part) return;
+  float *part = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.cols;
+  if (nrow == 1) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = threadIdx.x + k * blockDim.x;
-      if (c < nch) store8(p.dw_part + static_cast<int64_t>(blockIdx.x) * p.cols + c * 8, dw[k]);
+      if (c < nch) store8(part + c * 8, dw[k]);
+    }
+    return;
+  }
+  // the rows of the CTA in order, through the ring's memory (every copy into
+  // it has landed and been read)
+  float *sh = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = threadIdx.x + k * blockDim.x;
+    if (c < nch) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4 *>(sh + ty * p.cols + c * 8 + i) =
+            make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
     }
   }
-  ring_drain(&bars, stages, it);
+  __syncthreads();
+  for (int c = tid(); c < p.cols; c += blockDim.x * blockDim.y) {
+    float t = 0.0f;
+    for (int i = 0; i < nrow; ++i) t += sh[i * p.cols + c];
+    part[c] = t;
+  }
 }
 
 // dw[c] = sum over the parts, 32 columns per CTA: each of 32 warps takes every
@@ -603,34 +639,37 @@ inline dim3 norm_block(int cols, int ch) {
 constexpr int kMaxCtas = 8;  // per SM
 constexpr int kSmemPerSM = 233472 - 1024;  // shared memory of an SM, less one CTA's reserve
 
-// How a ring kernel goes over `rows` rows of `row_bytes` inputs: threads, CTAs
-// per SM, stages; ok = false where two stages do not fit or a thread would hold
-// more than two chunks.
+// How a ring kernel goes over `rows` rows of `row_bytes` inputs: threads per
+// row, rows per stage, CTAs per SM, stages; ok = false where two stages do not
+// fit or a thread would hold more than two chunks.  `threads_per_sm`: as many as
+// the kernel's registers allow; `several`: short rows go several to a stage, up
+// to 256 threads.
 struct RingPlan {
   bool ok;
-  int threads, per_sm, stages;
+  int threads, nrow, per_sm, stages;
   int smem;
   int64_t grid;
 };
-// `threads_per_sm`: as many as the kernel's registers allow.
-inline RingPlan ring_plan(int64_t rows, int cols, int64_t row_bytes, int threads_per_sm) {
+inline RingPlan ring_plan(int64_t rows, int cols, int64_t row_bytes, int threads_per_sm, bool several) {
   RingPlan p{};
   p.threads = (cols / 16 + 31) / 32 * 32;
   if (p.threads > 1024) return p;
-  int per_sm = threads_per_sm / p.threads;
+  p.nrow = several && p.threads <= 128 ? 256 / p.threads : 1;
+  const int64_t bytes = row_bytes * p.nrow;
+  int per_sm = threads_per_sm / (p.threads * p.nrow);
   if (per_sm > kMaxCtas) per_sm = kMaxCtas;
   if (per_sm < 1) per_sm = 1;
   // fewer CTAs, if that is what two stages take
-  while (per_sm > 1 && (2 * row_bytes + 1536) * per_sm > kSmemPerSM) --per_sm;
-  int64_t st = (kSmemPerSM / per_sm - 1536) / row_bytes;
+  while (per_sm > 1 && (2 * bytes + 1536) * per_sm > kSmemPerSM) --per_sm;
+  int64_t st = (kSmemPerSM / per_sm - 1536) / bytes;
   if (st > kRing) st = kRing;
   if (st < 2) return p;
   p.ok = true;
   p.per_sm = per_sm;
   p.stages = static_cast<int>(st);
-  p.smem = static_cast<int>(st * row_bytes);
-  const int64_t most = static_cast<int64_t>(moe_host::sm_count()) * per_sm;
-  p.grid = rows < most ? rows : most;
+  p.smem = static_cast<int>(st * bytes);
+  const int64_t most = static_cast<int64_t>(moe_host::sm_count()) * per_sm, want = (rows + p.nrow - 1) / p.nrow;
+  p.grid = want < most ? want : most;
   return p;
 }
 
@@ -648,8 +687,11 @@ cudaError_t launch_norm_rows(const NormFwd &p, cudaStream_t st) {
 template <typename TS, bool POW2>
 cudaError_t launch_norm_fwd(const NormFwd &p, cudaStream_t st) {
   const int64_t row_bytes = static_cast<int64_t>(p.cols) * sizeof(TS) * (p.resid ? 2 : 1);
-  const RingPlan pl = ring_plan(p.rows, p.cols, row_bytes, 1024);
-  if (pl.ok && p.rows >= 2 * pl.grid) {
+  // The ring pays where a CTA gets several rows of some length (T = 16384, bf16:
+  // 198 us against 329 at 7168 channels, 28 against 29 at 1024, 22 against 13 at
+  // 512).
+  const RingPlan pl = ring_plan(p.rows, p.cols, row_bytes, 1024, false);
+  if (pl.ok && p.cols > 1024 && p.rows >= 2 * pl.grid) {
     if (pl.threads <= 512) {
       static std::atomic<uint64_t> done{0};
       if (const cudaError_t e = smem_attr_once(add_rmsnorm_quant_ring_kernel<TS, POW2, 512, 2>, kSmemPerSM - 1536, done))
@@ -678,7 +720,7 @@ constexpr int kCh = 4;  // chunks a thread in the rows kernel
 
 template <typename TY, typename TS, typename TX>
 cudaError_t launch_norm_bwd(const NormBwd &p, int *parts, cudaStream_t st) {
-  const RingPlan pl = ring_plan(p.rows, p.cols, bwd_row_bytes<TY, TS>(p.cols, p.dres != nullptr), 512);
+  const RingPlan pl = ring_plan(p.rows, p.cols, bwd_row_bytes<TY, TS>(p.cols, p.dres != nullptr), 512, true);
   if (pl.ok) {
     *parts = static_cast<int>(pl.grid);
     if (pl.threads <= 512) {
@@ -686,7 +728,7 @@ cudaError_t launch_norm_bwd(const NormBwd &p, int *parts, cudaStream_t st) {
       if (const cudaError_t e = smem_attr_once(add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 512>, kSmemPerSM - 1536, done))
         return e;
       add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 512>
-          <<<static_cast<unsigned>(pl.grid), pl.threads, pl.smem, st>>>(p, pl.stages);
+          <<<static_cast<unsigned>(pl.grid), dim3(pl.threads, pl.nrow), pl.smem, st>>>(p, pl.stages);
     } else {
       static std::atomic<uint64_t> done{0};
       if (const cudaError_t e = smem_attr_once(add_rmsnorm_bwd_ring_kernel<TY, TS, TX, 1024>, kSmemPerSM - 1536, done))
@@ -699,7 +741,7 @@ cudaError_t launch_norm_bwd(const NormBwd &p, int *parts, cudaStream_t st) {
   // rows too long for two stages of the ring (above about 9000 FP32 channels)
   const int64_t most = 2 * static_cast<int64_t>(moe_host::sm_count());
   *parts = static_cast<int>(p.rows < most ? p.rows : most);
-  add_rmsnorm_bwd_kernel<TY, TS, TX, kCh><<<*parts, norm_block(p.cols, kCh), 0, st>>>(p);
+  add_rmsnorm_bwd_kernel<TY, TS, TX, kCh><<<*parts, dim3(norm_block(p.cols, kCh).x), 0, st>>>(p);  // a row a CTA
   return cudaGetLastError();
 }
 }  // namespace

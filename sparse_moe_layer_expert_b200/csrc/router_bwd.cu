@@ -14,7 +14,8 @@
 // three bf16 parts of 8 significand bits each (by truncation: the parts add up
 // to dz's 24 bits) and each product runs on the tensor cores once per part
 // into one FP32 accumulator: FP32-grade products at three bf16 passes.  Two
-// parts would leave an error of 2^-17 of each term.
+// parts, rounded to nearest, would leave 2^-16 of each term, 2.5e-6 of it in the
+// root mean square, where FP32 sums of a few thousand terms lose less than 1e-6.
 //
 // Kernels:
 //   router_dz_kernel   a warp per run of tokens: dz, written in FP32 (when asked

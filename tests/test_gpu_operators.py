@@ -412,3 +412,84 @@ def test_captured_replays_on_another_stream(m):
         for a, b in zip(got, w):
             assert torch.equal(a, b)
     assert m.moe_check_device_error(err)[0] == m.MOE_OK
+
+
+def test_many_short_sequences(m):
+    """More sequences than a grid's second dimension holds, most of them empty or one token long."""
+    T, Nr, Kr = 400, 16, 4
+    logits, idx = router_inputs(T, Nr, Kr, 1, 6)
+    cfg = m.config(128, 128, Nr, Kr)
+    off = torch.sort(torch.randint(0, T + 1, (70001,), generator=torch.Generator().manual_seed(0))).values
+    err = m.new_err_flag()
+    offd = off.to(torch.int32).cuda()
+    loss, counts = m.moe_balance_loss(cfg, logits.cuda(), idx.cuda(), offd, alpha=0.3, err=err)
+    z = logits.double().sum(0).numpy()
+    o = off.numpy()
+    lr, cr = O.balance_loss(z, idx.numpy().astype(np.int64), o, 0.3)
+    assert np.array_equal(counts.cpu().numpy(), cr)
+    assert (np.abs(f64(loss) - lr) <= (2 * z_tol(logits) + 60 * U) * lr).all()
+    dl, _, _ = m.moe_router_backward(cfg, logits.cuda(), idx.cuda(), dlogits=True, err=err,
+                                     balance=dict(seq_offsets=offd, counts=counts, alpha=0.3))
+    ref, mag = O.router_dlogits(z, idx.numpy().astype(np.int64), off=o, counts=cr, alpha=0.3)
+    assert (np.abs(f64(dl) - ref) <= (4 * z_tol(logits) + 40 * U) * mag + 1e-40).all()
+    assert m.moe_check_device_error(err)[0] == m.MOE_OK
+
+
+def test_on_a_stream_of_ones_own(m):
+    """A stream given by object or by handle: workspaces and outputs belong to it, results are the same."""
+    T, H, Nr, Kr = 300, 512, 16, 4
+    cfg = m.config(H, 128, Nr, Kr)
+    logits, idx = (t.cuda() for t in router_inputs(T, Nr, Kr, 2, 5))
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).cuda()
+    wr = (torch.randn((Nr, H), generator=g) * 0.02).to(torch.bfloat16).cuda()
+    dgate = torch.randn((T, Kr), generator=g).cuda()
+    off = torch.tensor([0, 100, 300], dtype=torch.int32).cuda()
+
+    def chain(**kw):
+        h, y, q, s, rstd = m.fp8_add_rmsnorm_quant_1x128(x, x, None, EPS, **kw)
+        loss, counts = m.moe_balance_loss(cfg, logits, idx, off, **kw)
+        _, dx, dwr = m.moe_router_backward(cfg, logits, idx, x=y, wr=wr, dgate=dgate, dx=True, dwr=True,
+                                           balance=dict(seq_offsets=off, counts=counts), **kw)
+        return [q, s, loss, dwr, *m.add_rmsnorm_backward(dx, h, rstd, **kw)]
+
+    want = chain()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for stream in (st, st.cuda_stream, 0):
+        for _ in range(3):
+            got = chain(stream=stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(m):
+    """Two calls of each kind under way at the same time keep their results."""
+    T, H, Nr, Kr = 2000, 1024, 64, 4
+    cfg = m.config(H, 128, Nr, Kr)
+    sets = []
+    for k in range(2):
+        g = torch.Generator().manual_seed(k)
+        logits, idx = (t.cuda() for t in router_inputs(T, Nr, Kr, 1, k))
+        sets.append((logits, idx, torch.randn((T, H), generator=g).to(torch.bfloat16).cuda(),
+                     (torch.randn((Nr, H), generator=g) * 0.02).to(torch.bfloat16).cuda(),
+                     torch.randn((T, Kr), generator=g).cuda()))
+
+    def chain(logits, idx, x, wr, dgate):
+        h, y, q, s, rstd = m.fp8_add_rmsnorm_quant_1x128(x, x, None, EPS)
+        _, dx, dwr = m.moe_router_backward(cfg, logits, idx, x=y, wr=wr, dgate=dgate, dx=True, dwr=True)
+        return [q, s, dwr, *m.add_rmsnorm_backward(dx, h, rstd)]
+
+    want = [chain(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k] = chain(*sets[k])
+    torch.cuda.synchronize()
+    for g_, w_ in zip(got, want):
+        for a, b in zip(g_, w_):
+            assert torch.equal(a, b)
