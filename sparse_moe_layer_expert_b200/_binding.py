@@ -19,7 +19,12 @@ LIB_PATH = os.path.join(_HERE, "libmoefp8.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python sparse_moe_layer_expert_b200/build.py`")
 
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
+if not os.path.exists(NATIVE_PATH):
+    raise ImportError(f"{NATIVE_PATH} is missing: build it with `python sparse_moe_layer_expert_b200/build.py`")
+
 lib = C.CDLL(LIB_PATH)
+from . import _native  # noqa: E402
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = -1
@@ -431,9 +436,7 @@ def moe_backward(cfg: MoeConfig, w: dict, wt: dict, x, dout, fwd_ws, dx=None, dW
 
 # ------------------------------------------- norm, balance loss, router
 # These calls check every tensor they are given (type, shape, device, strides)
-# and raise MoeError(MOE_ERR_INVALID_ARG) otherwise.  A decode step makes them
-# back to back, so the checks are written to cost little: one test per
-# property, the message only put together on the way out.
+# and raise MoeError(MOE_ERR_INVALID_ARG) otherwise.
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
@@ -505,6 +508,26 @@ def _scratch(fn, idx: int, *args) -> torch.Tensor:
     return torch.empty(n if n > 256 else 256, dtype=_U8, device=torch.device("cuda", idx))
 
 
+# The calls of a decode or training step go through _native (csrc/binding.cpp),
+# which checks their arguments, allocates what is not given and calls the C ABI.
+_native.init(MoeError, *(C.cast(getattr(lib, n), C.c_void_p).value for n in (
+    "fp8_add_rmsnorm_quant_1x128", "add_rmsnorm_backward_workspace_size", "add_rmsnorm_backward",
+    "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_router_backward_workspace_size",
+    "moe_router_backward")))
+
+
+def _launch(fn, t, *args):
+    """fn(current stream of t's device, *args) with that device current (the
+    library launches on the current device)."""
+    idx = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if idx < 0:
+        return fn(0, *args)  # which refuses it
+    if idx == torch._C._cuda_getDevice():
+        return fn(torch._C._cuda_getCurrentRawStream(idx), *args)
+    with torch.cuda.device(idx):
+        return fn(torch._C._cuda_getCurrentRawStream(idx), *args)
+
+
 def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: float = 1e-6, h=None, y=None, q=None,
                                 scales=None, rstd=None, pow2: bool = False, stream=None):
     """h = x + resid, y = h / rms(h) * weight, and y quantized 1x128, in one
@@ -514,42 +537,7 @@ def fp8_add_rmsnorm_quant_1x128(x: torch.Tensor, resid=None, weight=None, eps: f
     if stream is not None:
         with _use_stream(stream, x):
             return fp8_add_rmsnorm_quant_1x128(x, resid, weight, eps, h, y, q, scales, rstd, pow2)
-    where = "fp8_add_rmsnorm_quant_1x128"
-    code, idx = _stream_type(where, x, "x"), _cuda_index(where, x, "x")
-    shape = x.shape
-    if len(shape) != 2 or (shape[1] > 1 and x.stride(1) != 1):
-        _refuse(where, "x is [rows, cols] with unit stride along cols")
-    rows, cols = shape
-    dtype, dev = x.dtype, x.device
-    # a single row has no row stride
-    ld = ldr = cols
-    if rows > 1:
-        ld = x.stride(0)
-    rp = None
-    if resid is not None:
-        if (not isinstance(resid, torch.Tensor) or resid.dtype is not dtype or resid.get_device() != idx
-                or resid.shape != shape or (cols > 1 and resid.stride(1) != 1)):
-            _refuse(where, f"resid is not {dtype} {tuple(shape)} with unit stride along cols on CUDA device {idx}")
-        if rows > 1:
-            ldr = resid.stride(0)
-        rp = resid.data_ptr()
-        if h is None:
-            h = torch.empty(shape, dtype=dtype, device=dev)
-    if y is None:
-        y = torch.empty(shape, dtype=_BF16, device=dev)
-    if q is None:
-        q = torch.empty(shape, dtype=_U8, device=dev)
-    if scales is None:
-        scales = torch.empty((rows, cols // 128), dtype=_F32, device=dev)
-    if rstd is None:
-        rstd = torch.empty((rows,), dtype=_F32, device=dev)
-    _on_device(lib.fp8_add_rmsnorm_quant_1x128, idx, where, (
-        x.data_ptr(), ld, rp, ldr, code, None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
-        eps, rows, cols, None if h is None else _want(where, h, "h", dtype, shape, idx),
-        _want(where, y, "y", _BF16, shape, idx), _want(where, q, "q", _U8, shape, idx),
-        _want(where, scales, "scales", _F32, (rows, cols // 128), idx), _want(where, rstd, "rstd", _F32, (rows,), idx),
-        MOE_SCALE_POW2 if pow2 else MOE_SCALE_AMAX))
-    return x if h is None else h, y, q, scales, rstd
+    return _launch(_native.norm_fwd, x, x, resid, weight, eps, h, y, q, scales, rstd, pow2)
 
 
 def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, dx_dtype=None, ws=None, stream=None):
@@ -560,29 +548,7 @@ def add_rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dw=None, 
     if stream is not None:
         with _use_stream(stream, h):
             return add_rmsnorm_backward(dy, h, rstd, weight, dres, dx, dw, dx_dtype, ws)
-    where = "add_rmsnorm_backward"
-    code, idx = _stream_type(where, h, "h"), _cuda_index(where, h, "h")
-    shape, dtype = h.shape, h.dtype
-    if len(shape) != 2:
-        _refuse(where, "h is [rows, cols]")
-    rows, cols = shape
-    ycode = _stream_type(where, dy, "dy")
-    if dx is None:
-        dx = torch.empty(shape, dtype=dx_dtype or dtype, device=h.device)
-    elif dx_dtype is not None and dx.dtype is not dx_dtype:
-        _refuse(where, f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
-    xcode = _stream_type(where, dx, "dx")
-    if dw is None:
-        dw = torch.empty((cols,), dtype=_F32, device=h.device)
-    if ws is None:
-        ws = _scratch(lib.add_rmsnorm_backward_workspace_size, idx, rows, cols)
-    _on_device(lib.add_rmsnorm_backward, idx, where, (
-        _want(where, dy, "dy", dy.dtype, shape, idx), ycode, _want(where, h, "h", dtype, shape, idx),
-        None if dres is None else _want(where, dres, "dres", dtype, shape, idx), code,
-        None if weight is None else _want(where, weight, "weight", _F32, (cols,), idx),
-        _want(where, rstd, "rstd", _F32, (rows,), idx), rows, cols, _want(where, dx, "dx", dx.dtype, shape, idx), xcode,
-        _want(where, dw, "dw", _F32, (cols,), idx), _want(where, ws, "ws", _U8, None, idx), ws.numel()))
-    return dx, dw
+    return _launch(_native.norm_bwd, h, dy, h, rstd, weight, dres, dx, dw, dx_dtype, ws)
 
 
 def moe_router_splits(cfg: MoeConfig, T: int) -> int:
@@ -600,25 +566,6 @@ def moe_route_logits(cfg: MoeConfig, T: int, ws: torch.Tensor) -> torch.Tensor:
     return ws[:n * T * cfg.n_routed * 4].view(torch.float32).view(n, T, cfg.n_routed)
 
 
-def _router_state(where: str, cfg: MoeConfig, logits, picks):
-    """(n_splits, T, device, logits pointer, picks pointer)"""
-    idx = _cuda_index(where, logits, "logits")
-    shape = logits.shape
-    if len(shape) != 3 or shape[0] < 1 or shape[2] != cfg.n_routed:
-        _refuse(where, f"logits is {tuple(shape)}, wanted [n_splits, T, {cfg.n_routed}]")
-    return (shape[0], shape[1], idx, _want(where, logits, "logits", _F32, None, idx),
-            _want(where, picks, "idx", _I32, (shape[1], cfg.top_k), idx))
-
-
-def _sequences(where: str, off, idx: int):
-    """(n_seq, pointer) of the offsets of packed sequences."""
-    p = _want(where, off, "seq_offsets", _I32, None, idx)
-    shape = off.shape
-    if len(shape) != 1 or shape[0] < 1:
-        _refuse(where, "seq_offsets is [n_seq + 1]")
-    return shape[0] - 1, p
-
-
 def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e-4, loss=None, counts=None, ws=None,
                      err=None, stream=None):
     """Sequence-wise balance loss and per-expert counts of packed sequences:
@@ -628,31 +575,8 @@ def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e
     if stream is not None:
         with _use_stream(stream, logits):
             return moe_balance_loss(cfg, logits, idx, seq_offsets, alpha, loss, counts, ws, err)
-    where = "moe_balance_loss"
-    n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
-    n_seq, op = _sequences(where, seq_offsets, dev)
-    if loss is None:
-        loss = torch.empty((n_seq,), dtype=_F32, device=logits.device)
-    if counts is None:
-        counts = torch.empty((n_seq, cfg.n_routed), dtype=_I32, device=logits.device)
-    cp = C.byref(cfg)
-    if ws is None:
-        ws = _scratch(lib.moe_balance_loss_workspace_size, dev, cp, T, n_seq)
-    if err is None:
-        err = new_err_flag(logits.device)
-    _on_device(lib.moe_balance_loss, dev, where, (
-        cp, zp, n, ip, T, op, n_seq, alpha, _want(where, loss, "loss", _F32, (n_seq,), dev),
-        _want(where, counts, "counts", _I32, (n_seq, cfg.n_routed), dev), _want(where, ws, "ws", _U8, None, dev),
-        ws.numel(), _want(where, err, "err", _I32, None, dev)))
-    return loss, counts
-
-
-def _balance_struct(where: str, cfg: MoeConfig, b: dict, idx: int) -> MoeBalanceGrad:
-    n_seq, op = _sequences(where, b["seq_offsets"], idx)
-    dloss = b.get("dloss")
-    return MoeBalanceGrad(op, n_seq, b.get("alpha", 1e-4),
-                          _want(where, b["counts"], "counts", _I32, (n_seq, cfg.n_routed), idx),
-                          None if dloss is None else _want(where, dloss, "dloss", _F32, (n_seq,), idx))
+    return _launch(_native.balance_loss, logits, C.addressof(cfg), logits, idx, seq_offsets, alpha, loss, counts, ws,
+                   err)
 
 
 def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None, balance=None, dlogits=None, dx=None,
@@ -665,36 +589,27 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
     dwr, wr bf16 [N_r, H] for dx.  dx_accumulate adds to dx."""
     if stream is not None:
         with _use_stream(stream, logits):
-            return moe_router_backward(cfg, logits, idx, x, wr, dgate, balance, dlogits, dx, dx_accumulate, dwr, ws, err)
-    where = "moe_router_backward"
-    n, T, dev, zp, ip = _router_state(where, cfg, logits, idx)
-    H, Nr = cfg.hidden, cfg.n_routed
-    if dx_accumulate and (dx is None or dx is True or dx is False):
-        _refuse(where, "dx_accumulate needs a dx to add to")
+            return moe_router_backward(cfg, logits, idx, x, wr, dgate, balance, dlogits, dx, dx_accumulate, dwr, ws,
+                                       err)
+    return _launch(_native.router_backward, logits, C.addressof(cfg), logits, idx, x, wr, dgate, balance, dlogits, dx,
+                   dx_accumulate, dwr, ws, err)
 
-    def out(t, name, shape):
-        if t is None or t is False:
-            return None, None
-        if t is True:
-            t = torch.empty(shape, dtype=_F32, device=logits.device)
-        return t, _want(where, t, name, _F32, shape, dev)
 
-    dlogits, lp = out(dlogits, "dlogits", (T, Nr))
-    dx, xp = out(dx, "dx", (T, H))
-    dwr, wp = out(dwr, "dwr", (Nr, H))
-    cp = C.byref(cfg)
-    if ws is None and (dx is not None or dwr is not None):
-        ws = _scratch(lib.moe_router_backward_workspace_size, dev, cp, T)
-    if err is None:
-        err = new_err_flag(logits.device)
-    _on_device(lib.moe_router_backward, dev, where, (
-        cp, zp, n, ip, T, None if dgate is None else _want(where, dgate, "dgate", _F32, (T, cfg.top_k), dev),
-        None if balance is None else C.byref(_balance_struct(where, cfg, balance, dev)),
-        None if x is None and dwr is None else _want(where, x, "x", _BF16, (T, H), dev),
-        None if wr is None and dx is None else _want(where, wr, "wr", _BF16, (Nr, H), dev), lp, xp,
-        1 if dx_accumulate else 0, wp, None if ws is None else _want(where, ws, "ws", _U8, None, dev),
-        0 if ws is None else ws.numel(), _want(where, err, "err", _I32, None, dev)))
-    return dlogits, dx, dwr
+def _sequences(where: str, off, idx: int):
+    """(n_seq, pointer) of the offsets of packed sequences."""
+    p = _want(where, off, "seq_offsets", _I32, None, idx)
+    shape = off.shape
+    if len(shape) != 1 or shape[0] < 1:
+        _refuse(where, "seq_offsets is [n_seq + 1]")
+    return shape[0] - 1, p
+
+
+def _balance_struct(where: str, cfg: MoeConfig, b: dict, idx: int) -> MoeBalanceGrad:
+    n_seq, op = _sequences(where, b["seq_offsets"], idx)
+    dloss = b.get("dloss")
+    return MoeBalanceGrad(op, n_seq, b.get("alpha", 1e-4),
+                          _want(where, b["counts"], "counts", _I32, (n_seq, cfg.n_routed), idx),
+                          None if dloss is None else _want(where, dloss, "dloss", _F32, (n_seq,), idx))
 
 
 def moe_block_forward(cfg: MoeConfig, w: dict, bias, x, resid=None, norm_weight=None, eps: float = 1e-6, h=None, y=None,

@@ -7,7 +7,9 @@
 Compiles every csrc/*.cu with nvcc for compute_100a/sm_100a into one shared
 library next to this file.  The CUDA runtime is linked statically and the
 driver API is reached through cudaGetDriverEntryPoint, so the library loads
-(and exports its symbols) on a machine without a GPU driver.
+(and exports its symbols) on a machine without a GPU driver.  csrc/binding.cpp
+becomes _native.so, the Python side of the operators around the layer (torch's
+own C++ headers and libraries; g++).
 """
 from __future__ import annotations
 
@@ -19,8 +21,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoefp8.so")
+NATIVE = os.path.join(HERE, "_native.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -66,6 +70,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_native(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "moe_fp8.h")]
+    if not force and os.path.exists(NATIVE) and all(os.path.getmtime(d) <= os.path.getmtime(NATIVE) for d in deps):
+        return NATIVE
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    lib = os.path.join(t, "lib")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                    "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
+                    "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), src, "-o", tmp, "-L", lib,
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"], check=True)
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 if __name__ == "__main__":
+    build_native(force="--force" in sys.argv)
     build(force="--force" in sys.argv, verbose="--verbose" in sys.argv)
     print(LIB)

@@ -271,6 +271,15 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
   float ss = 0.0f;
   const TS *x = static_cast<const TS *>(p.x) + r * p.ld_x;
   const TS *rs = p.resid ? static_cast<const TS *>(p.resid) + r * p.ld_r : nullptr;
+  // the weight: with one chunk a thread asked for with the row (few rows: its
+  // latency would stand alone behind the row's sum), else where it is used
+  auto weight = [&](int c, bool in, float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (in && p.w) load8(p.w + c * 8, w);
+  };
+  float w0[8];
+  if (CH == 1) weight(threadIdx.x, live && static_cast<int>(threadIdx.x) < nch, w0);
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = threadIdx.x + k * blockDim.x;
@@ -287,12 +296,13 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
     const int c = threadIdx.x + k * blockDim.x;
     const bool in = live && c < nch;
     float w[8];
+    if (CH == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-    if (in) {
-      if (p.h) store_h(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k], hc[k]);
-      if (p.w) load8(p.w + c * 8, w);
+      for (int i = 0; i < 8; ++i) w[i] = w0[i];
+    } else {
+      weight(c, in, w);
     }
+    if (in && p.h) store_h(static_cast<TS *>(p.h) + r * p.cols + c * 8, f[k], hc[k]);
     finish_chunk<POW2>(f[k], w, rstd, in, p.y ? p.y + r * p.cols + c * 8 : nullptr, p.q + r * p.cols + c * 8,
                        p.s + r * (p.cols / 128) + (c >> 4));
   }
