@@ -493,3 +493,74 @@ def test_two_streams_at_once(m):
     for g_, w_ in zip(got, want):
         for a, b in zip(g_, w_):
             assert torch.equal(a, b)
+
+
+def test_router_outputs_at_their_least_alignment(m):
+    """dx and dwr 16 bytes into a sector, dlogits and its inputs on odd words: the same bits as aligned ones."""
+    T, H, Nr, Kr = 300, 384, 100, 5
+    cfg = m.config(H, 128, Nr, Kr)
+    logits, idx = (t.cuda() for t in router_inputs(T, Nr, Kr, 2, 8))
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).cuda()
+    wr = (torch.randn((Nr, H), generator=g) * 0.02).to(torch.bfloat16).cuda()
+    dgate = torch.randn((T, Kr), generator=g).cuda()
+
+    def off(n, shape, src=None, dtype=torch.float32):
+        size = int(np.prod(shape))
+        t = torch.empty(size + n, dtype=dtype, device="cuda")[n:].view(shape)
+        return t if src is None else t.copy_(src)
+
+    want = m.moe_router_backward(cfg, logits, idx, x=x, wr=wr, dgate=dgate, dlogits=True, dx=True, dwr=True)
+    dx, dwr, dl = off(4, (T, H)), off(4, (Nr, H)), off(1, (T, Nr))
+    assert dx.data_ptr() % 32 == 16 and dl.data_ptr() % 16 == 4
+    got = m.moe_router_backward(cfg, off(4, logits.shape, logits), off(1, idx.shape, idx, torch.int32),
+                                x=off(8, x.shape, x, torch.bfloat16), wr=off(8, wr.shape, wr, torch.bfloat16),
+                                dgate=off(1, dgate.shape, dgate), dlogits=dl, dx=dx, dwr=dwr)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    # logits off a 16-byte boundary are refused
+    with pytest.raises(m.MoeError):
+        m.moe_router_backward(cfg, off(1, logits.shape, logits), idx, dgate=dgate, dlogits=True)
+
+
+def test_bindings_refuse_wrong_tensors(m):
+    T, H, Nr, Kr = 4, 256, 16, 4
+    cfg = m.config(H, 128, Nr, Kr)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    f = torch.zeros((T, H), device="cuda")
+    r = torch.ones(T, device="cuda")
+    z, idx = torch.zeros((1, T, Nr), device="cuda"), torch.zeros((T, Kr), dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    wr = torch.zeros((Nr, H), dtype=torch.bfloat16, device="cuda")
+    n, b, l, w = m.fp8_add_rmsnorm_quant_1x128, m.add_rmsnorm_backward, m.moe_balance_loss, m.moe_router_backward
+    counts = torch.zeros((1, Nr), dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: n(x.half()), lambda: n(x.t()), lambda: n(x[0]), lambda: n(x, f), lambda: n(x, x[:2]),
+        lambda: n(x, x.cpu()), lambda: n(x, None, torch.ones(H, device="cuda", dtype=torch.bfloat16)),
+        lambda: n(x, None, torch.ones(H)), lambda: n(x, y=f), lambda: n(x, q=torch.zeros((T, H), device="cuda")),
+        lambda: n(x, scales=torch.zeros((T, 3), device="cuda")), lambda: n(x, rstd=torch.zeros(T + 1, device="cuda")),
+        lambda: n(x, x, h=f), lambda: n(x[:, :250]), lambda: n(None), lambda: n(x, eps=0.0), lambda: n(x[:, 1:129]),
+        lambda: b(f, x, r[:2]), lambda: b(f.half(), x, r), lambda: b(f, x, r, dres=f), lambda: b(f, x, r, dx=f.half()),
+        lambda: b(f, x, r, dx=f, dx_dtype=torch.bfloat16), lambda: b(f, x.t(), r), lambda: b(f[:2], x, r),
+        lambda: b(f, x, r, ws=torch.zeros(8, dtype=torch.uint8, device="cuda")), lambda: b(f, x, r, dx_dtype=torch.half),
+        lambda: b(f, x, r, dw=torch.zeros(H + 1, device="cuda")), lambda: b(f, x, r, dx_dtype="bf16"),
+        lambda: l(cfg, z[0], idx, off), lambda: l(cfg, z, idx.long(), off), lambda: l(cfg, z, idx, off.long()),
+        lambda: l(cfg, z, idx[:2], off), lambda: l(cfg, z, idx, off[:0]), lambda: l(cfg, z[:, :, :8], idx, off),
+        lambda: l(cfg, z, idx, off, loss=r), lambda: l(cfg, z, idx, off, alpha=float("nan")),
+        lambda: l(cfg, z, idx, off, counts=torch.zeros((1, Nr), device="cuda")),
+        lambda: w(cfg, z, idx, dwr=True), lambda: w(cfg, z, idx, dx=True), lambda: w(cfg, z, idx, x=f, dwr=True),
+        lambda: w(cfg, z, idx, dgate=f, dlogits=True), lambda: w(cfg, z, idx, wr=wr, dx=True, dx_accumulate=True),
+        lambda: w(cfg, z, idx, dlogits=f), lambda: w(cfg, z, idx, balance=dict(seq_offsets=off), dlogits=True),
+        lambda: w(cfg, z, idx, balance=dict(seq_offsets=off, counts=counts[:, :8]), dlogits=True),
+        lambda: w(cfg, z, idx, balance=dict(seq_offsets=off, counts=counts, dloss=f), dlogits=True),
+        lambda: w(cfg, z, idx, balance=[off, counts], dlogits=True),
+        lambda: w(cfg, z, idx, wr=wr, dx=True, ws=torch.zeros(8, dtype=torch.uint8, device="cuda")),
+    ]
+    for i, f_ in enumerate(bad):
+        with pytest.raises(m.MoeError):
+            f_()
+            pytest.fail(f"case {i} was not refused")
+    # and what is asked for in its least form works
+    assert w(cfg, z, idx) == (None, None, None)
+    assert w(cfg, z, idx, wr=wr, dx=True)[1].abs().sum() == 0
+    torch.cuda.synchronize()
