@@ -266,8 +266,9 @@ struct RouterBwd {
 int router_parts_pitch(int Nr);
 size_t router_dwr_scratch(int64_t T, int cols);  // bytes of launch_router_dwr's part
 cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st);
+// beside_dwr: launch_router_dwr comes directly behind it and shares the SMs
 cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
-                             int32_t *err, uint64_t limit_ns, cudaStream_t st);
+                             bool beside_dwr, int32_t *err, uint64_t limit_ns, cudaStream_t st);
 // behind_dx: launch_router_dx came directly before it on the stream (else launch_router_dz)
 cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
                               bool behind_dx, int32_t *err, uint64_t limit_ns, cudaStream_t st);

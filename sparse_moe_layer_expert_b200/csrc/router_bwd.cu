@@ -273,12 +273,13 @@ __host__ __device__ inline PairUnits pair_units(int pair, int pairs, int units) 
 // them.  The parts are three times the bytes of W_r's strip, so they are what
 // stays: a token tile's parts (Np experts x 128 tokens x 3 in each CTA, 192 KB)
 // stay in shared memory over its strips while W_r streams past in stages of 32
-// experts (half a strip's columns in each CTA), 64 KB a unit against 192 KB
-// the other way round (T = 4096, N_r = 256, H = 7168: 43 us that way, 39 us this,
-// where the products alone take 28 us at the library's matrix rate).  The next tile's parts arrive as the current one's last pass over
-// each 64-expert block ends.  The epilogue turns TMEM's
-// rows so that four lanes store 128 contiguous bytes of a row (a row per thread
-// took 64 cycles an instruction in the L1).
+// experts (half a strip's columns in each CTA), 64 KB a unit against 192 KB the
+// other way round (T = 4096, N_r = 256, H = 7168, alone on the device: 43 us that
+// way, 39 us this, where the products take 28 us at the library's matrix rate and
+// the output 30 us at the card's write rate).  The next tile's parts arrive as the
+// current one's last pass over each 64-expert block ends.  The epilogue turns
+// TMEM's rows so that four lanes store 128 contiguous bytes of a row (a row per
+// thread took 64 cycles an instruction in the L1).
 constexpr int X_STAGES = 4;
 constexpr int X_THREADS = 320;        // warp 0 TMA, warp 1 MMA (even CTA), warps 2..9 epilogue
 constexpr int X_AB = 128 * 128;       // 128 tokens x 64 experts, one part
@@ -548,14 +549,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
 }
 
 // ------------------------------------------------------------ dW_r = dz^T x
-// Units (256-column strip of x, 64-token stage), strip-major; a pair takes a
-// run of them, so a strip's tokens are shared out over several pairs and every
-// SM has the same work.  The tensor core's FP32 accumulation drops the bits
+// Units (256-column strip of x, 64-token stage), strip-major, in as many equal runs
+// as the device has pairs; a pair takes one run, or where router_dx_kernel has
+// the other half of the SMs, two.  A strip's tokens are so shared out over several
+// runs and every SM has the same work.  The tensor core's FP32 accumulation drops the bits
 // below its 24 at every step (measured: the error grows with the number of
 // steps, to 6e-6 of the result over 3300 tokens), so one TMEM accumulator takes
 // WR_CHUNK stages (24 steps) at most: the epilogue warps add it into FP32
 // registers while the next chunk's MMAs fill the other buffer.  At the end of a
-// strip's run the registers go to the partial sums, piece (pair + strip).
+// strip's run the registers go to the partial sums, piece (run + strip).
 // A stage is two loads, one 4D box of the parts and one 3D box of x: as eight
 // 2D boxes of 32 tokens each load cost about 110 ns and set the pace.
 namespace {
@@ -581,7 +583,8 @@ struct DwrArgs {
   int64_t T;
   int n_strips, n_stages;  // H / 256 and T / 64, rounded up
   int Nr;
-  float *part;             // [pairs + n_strips, 256, 256]
+  int n_runs;              // what the units are shared out to
+  float *part;             // [n_runs + n_strips, 256, 256]
   int behind_dx;           // launched behind router_dx_kernel, not router_dz_kernel
   int32_t *err;
   uint64_t limit_ns;
@@ -631,8 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   const uint32_t tmem = bars->tmem_base;
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
-  const int pair = blockIdx.x >> 1;
-  const PairUnits pu = pair_units(pair, gridDim.x >> 1, args.n_strips * args.n_stages);
+  // this pair's share [r0, r1) of the runs that the units fall into
+  const PairUnits runs = pair_units(blockIdx.x >> 1, gridDim.x >> 1, args.n_runs);
+  const int units = args.n_strips * args.n_stages;
 
   dependents_start();
   if (!args.behind_dx) predecessor_done();
@@ -645,7 +649,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
         const uint64_t pol_a = policy_evict_last();   // every strip reads the parts again
         const uint64_t pol_x = policy_evict_first();  // x is read once
         uint32_t it = 0;
-        for (int u = pu.u0; u < pu.u1; ++u, ++it) {
+        // the runs follow each other: one range of units
+        const int u1 = runs.u1 > runs.u0 ? pair_units(runs.u1 - 1, args.n_runs, units).u1 : 0;
+        for (int u = pair_units(runs.u0, args.n_runs, units).u0; u < u1; ++u, ++it) {
           const int s = it % WR_STAGES;
           if (*abortp || !mbar_wait(&bars->empty[s], ((it / WR_STAGES) & 1) ^ 1, ctl)) break;
           uint8_t *st = smem + s * WR_STAGE;
@@ -666,34 +672,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
         uint32_t it = 0, tc = 0;
         bool stop = false;
         const uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescAMn | kIdescBMn;
-        for (int u = pu.u0; u < pu.u1 && !stop;) {
-          const int end = run_end(u, pu.u1, args.n_stages);
-          for (; u < end && !stop; ++tc) {
-            const uint32_t buf = tc & 1;
-            if (*abortp || !mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) {
-              stop = true;
-              break;
-            }
-            const uint32_t d = tmem + buf * 256;
-            for (int k = 0; k < WR_CHUNK && u < end; ++k, ++u, ++it) {
-              const int s = it % WR_STAGES;
-              if (!mbar_wait(&bars->full[s], (it / WR_STAGES) & 1, ctl)) {
+        for (int run = runs.u0; run < runs.u1 && !stop; ++run) {
+          const PairUnits pu = pair_units(run, args.n_runs, units);
+          for (int u = pu.u0; u < pu.u1 && !stop;) {
+            const int end = run_end(u, pu.u1, args.n_stages);
+            for (; u < end && !stop; ++tc) {
+              const uint32_t buf = tc & 1;
+              if (*abortp || !mbar_wait(&bars->tempty[buf], ((tc >> 1) & 1) ^ 1, ctl)) {
                 stop = true;
                 break;
               }
-              tc_fence_after();
-              const uint32_t st = smem_u32(smem + s * WR_STAGE);
+              const uint32_t d = tmem + buf * 256;
+              for (int k = 0; k < WR_CHUNK && u < end; ++k, ++u, ++it) {
+                const int s = it % WR_STAGES;
+                if (!mbar_wait(&bars->full[s], (it / WR_STAGES) & 1, ctl)) {
+                  stop = true;
+                  break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * WR_STAGE);
 #pragma unroll
-              for (int q = 0; q < WR_TOK / 16; ++q) {
-                const uint64_t db = sw128_mnmajor_desc(st + WR_A + q * 2048, WR_G);
+                for (int q = 0; q < WR_TOK / 16; ++q) {
+                  const uint64_t db = sw128_mnmajor_desc(st + WR_A + q * 2048, WR_G);
 #pragma unroll
-                for (int p = 0; p < kParts; ++p)
-                  umma_bf16_pair(d, sw128_mnmajor_desc(st + p * 2 * WR_G + q * 2048, WR_G), db, idesc,
-                                 (k > 0 || q > 0 || p > 0) ? 1u : 0u);
+                  for (int p = 0; p < kParts; ++p)
+                    umma_bf16_pair(d, sw128_mnmajor_desc(st + p * 2 * WR_G + q * 2048, WR_G), db, idesc,
+                                   (k > 0 || q > 0 || p > 0) ? 1u : 0u);
+                }
+                umma_commit_pair(&bars->empty[s], 0x3);
               }
-              umma_commit_pair(&bars->empty[s], 0x3);
+              umma_commit_pair(&bars->tfull[buf], 0x3);
             }
-            umma_commit_pair(&bars->tfull[buf], 0x3);
           }
         }
         int quiet = 0;
@@ -709,64 +718,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
     const bool live = rank * 128 + q * 32 < args.Nr;     // any expert in this warp
     uint32_t tc = 0;
     bool stop = false;
-    for (int u = pu.u0; u < pu.u1 && !stop;) {
-      const int strip = u / args.n_stages;
-      const int end = run_end(u, pu.u1, args.n_stages);
-      // 16-row halves h, 32-column blocks c: lane 4 i + j holds rows i, i + 8 and
-      // columns 2 j, 2 j + 1 of each 8-column block (tmem_ld_16x256)
-      float acc[2][4][16];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
-      for (; u < end; u += WR_CHUNK, ++tc) {
-        const uint32_t buf = tc & 1;
-        if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) {
-          stop = true;
-          break;
-        }
-        if (live) {
-          tc_fence_after();
-          const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[2][16];
-            tmem_ld_16x256(ta + c * 32, v[0]);
-            tmem_ld_16x256(ta + c * 32 + (1 << 20), v[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) acc[h][c][j] += __uint_as_float(v[h][j]);
-          }
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
-      }
-      if (live) {
+    for (int run = runs.u0; run < runs.u1 && !stop; ++run) {
+      const PairUnits pu = pair_units(run, args.n_runs, units);
+      for (int u = pu.u0; u < pu.u1 && !stop;) {
+        const int strip = u / args.n_stages;
+        const int end = run_end(u, pu.u1, args.n_stages);
+        // 16-row halves h, 32-column blocks c: lane 4 i + j holds rows i, i + 8 and
+        // columns 2 j, 2 j + 1 of each 8-column block (tmem_ld_16x256)
+        float acc[2][4][16];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r8 = 0; r8 < 2; ++r8) {
-            const int row = rank * 128 + q * 32 + h * 16 + r8 * 8 + (lane >> 2);  // expert
-            float *o = args.part + (static_cast<int64_t>(pair + strip) * 256 + row) * 256 + wg * 128 + (lane & 3) * 8;
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
+        for (; u < end; u += WR_CHUNK, ++tc) {
+          const uint32_t buf = tc & 1;
+          if (!mbar_wait(&bars->tfull[buf], (tc >> 1) & 1, ctl)) {
+            stop = true;
+            break;
+          }
+          if (live) {
+            tc_fence_after();
+            const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + wg * 128;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              float f[8];
+              uint32_t v[2][16];
+              tmem_ld_16x256(ta + c * 32, v[0]);
+              tmem_ld_16x256(ta + c * 32 + (1 << 20), v[1]);
+              tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                f[2 * j] = acc[h][c][4 * j + 2 * r8];
-                f[2 * j + 1] = acc[h][c][4 * j + 2 * r8 + 1];
-              }
-              quad_transpose(f, lane);
-              if (row < args.Nr) st_f32x8(o + c * 32, f);
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[h][c][j] += __uint_as_float(v[h][j]);
             }
+            tc_fence_before();
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars->tempty[buf]), 0));
+        }
+        if (live) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r8 = 0; r8 < 2; ++r8) {
+              const int row = rank * 128 + q * 32 + h * 16 + r8 * 8 + (lane >> 2);  // expert
+              float *o = args.part + (static_cast<int64_t>(run + strip) * 256 + row) * 256 + wg * 128 + (lane & 3) * 8;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  f[2 * j] = acc[h][c][4 * j + 2 * r8];
+                  f[2 * j + 1] = acc[h][c][4 * j + 2 * r8 + 1];
+                }
+                quad_transpose(f, lane);
+                if (row < args.Nr) st_f32x8(o + c * 32, f);
+              }
+            }
+        }
+        u = end;
       }
-      u = end;
     }
   }
   tc_fence_before();
@@ -779,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
 
 // dW_r [Nr, cols] from the pieces of each strip, in token order.  CTA (4
 // experts, strip): 64 threads of 4 columns for each expert.  A strip has
-// pairs / n_strips + 2 pieces at most; four are read at once.
+// runs / n_strips + 2 pieces at most; four are read at once.
 __global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__ part, int pairs, int n_strips,
                                                         int n_stages, int Nr, int cols, float *__restrict__ out) {
   const int strip = blockIdx.y;
@@ -831,6 +843,15 @@ int dwr_pairs(int64_t T, int cols) {
 }
 }  // namespace
 
+// Whether dx and dW_r, both asked for, run side by side on half of the SMs each:
+// dx alone is held up by its stores and dW_r by its loads, but with many units a
+// pair both reach the matrix rate by themselves.  (H = 7168, N_r = 256, a pass:
+// T = 512 32.4 us one after the other, 30.7 side by side; 2048 53.6, 49.3; 4096
+// 78.7, 77.3; 8192 139, 141; 16381 265, 273.)
+static bool share_sms(int64_t T, int cols) {
+  return static_cast<int64_t>(strips_of(cols)) * ((T + 255) / 256) < 12 * most_pairs();
+}
+
 size_t router_dwr_scratch(int64_t T, int cols) {
   return T == 0 ? 0 : static_cast<size_t>(dwr_pairs(T, cols) + strips_of(cols)) * 256 * 256 * sizeof(float);
 }
@@ -870,7 +891,7 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
 }
 
 cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
-                             int32_t *err, uint64_t limit_ns, cudaStream_t st) {
+                             bool beside_dwr, int32_t *err, uint64_t limit_ns, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
   const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
   // in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], W_r [H / 64][Nr][64]
@@ -896,6 +917,7 @@ cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int N
   const int units = a.n_strips * a.m_tiles;
   static std::atomic<int> resident[64];
   int64_t pairs = resident_pairs(router_dx_kernel, X_THREADS, X_SMEM, most_pairs(), resident);
+  if (beside_dwr && share_sms(T, H)) pairs = (pairs + 1) / 2;
   if (pairs > units) pairs = units;
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
   return launch_next(router_dx_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(X_THREADS), X_SMEM, st, ma, mw, a);
@@ -925,14 +947,21 @@ cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int N
   static std::atomic<uint64_t> attr_done{0};
   if (const cudaError_t e = smem_attr_once(router_dwr_kernel, WR_SMEM, attr_done)) return e;
   static std::atomic<int> resident[64];
-  int64_t pairs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident);
-  if (pairs > dwr_pairs(T, H)) pairs = dwr_pairs(T, H);
-  if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  int64_t runs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident);
+  if (runs > dwr_pairs(T, H)) runs = dwr_pairs(T, H);
+  if (runs < 1) return cudaErrorLaunchOutOfResources;
+  a.n_runs = static_cast<int>(runs);
+  // beside dx, half of the pairs take two runs each, where the runs need them
+  int64_t pairs = runs;
+  if (behind_dx && share_sms(T, H)) {
+    const int64_t left = most_pairs() - (most_pairs() + 1) / 2;
+    if (pairs > left) pairs = (runs + 1) / 2;
+  }
   cudaError_t e = launch_next(router_dwr_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(WR_THREADS), WR_SMEM, st,
                               ma, mx, a);
   if (e != cudaSuccess) return e;
   return launch_next(dwr_join_kernel, dim3(static_cast<unsigned>((Nr + 3) / 4), static_cast<unsigned>(a.n_strips)),
-                     dim3(256), 0, st, static_cast<const float *>(part), static_cast<int>(pairs), a.n_strips, a.n_stages,
+                     dim3(256), 0, st, static_cast<const float *>(part), a.n_runs, a.n_strips, a.n_stages,
                      Nr, H, dwr);
 }
 
