@@ -89,7 +89,8 @@ def test_block_forward(m, T, over):
 
 
 @pytest.mark.parametrize("T,over,off", [(300, {}, [0, 100, 100, 290]), (1, {}, None), (129, dict(route_scale=2.5), [0, 129]),
-                                        (70, dict(Ns=0), None), (200, dict(n_groups=4, topk_groups=2), [0, 64, 200])])
+                                        (70, dict(Ns=0), None), (200, dict(n_groups=4, topk_groups=2), [0, 64, 200]),
+                                        (600, dict(H=1152, I=384, Nr=72, Kr=8), [0, 5, 400, 600])])
 def test_block_backward(m, T, over, off):
     cfg, layer, x, resid, w, dout = problem(m, T, 5, **over)
     layer.cfg.route_scale = over.get("route_scale", 1.0)
