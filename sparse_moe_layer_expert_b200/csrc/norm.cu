@@ -241,6 +241,18 @@ __device__ __forceinline__ void finish_chunk(float (&f)[8], const float (&w)[8],
   }
 }
 
+// 1 / sqrt(ss / cols + eps): the hardware's reciprocal square root r of v and one
+// Newton step r + r (1 - v r^2) / 2 with v r taken to twice FP32's digits, which
+// leaves about half an FP32 step (1.0f / sqrtf(v) rounds twice).
+__device__ __forceinline__ float rstd_of(float ss, int cols, float eps) {
+  const float v = ss / static_cast<float>(cols) + eps;
+  const float r = rsqrtf(v);
+  if (!(v <= 3.402823466e38f)) return r;  // infinity gives 0, NaN itself
+  const float p = v * r;
+  const float h = fmaf(-fmaf(v, r, -p), r, fmaf(-p, r, 1.0f));
+  return fmaf(0.5f * h, r, r);
+}
+
 struct NormFwd {
   const void *x, *resid;
   int64_t ld_x, ld_r;
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_quant_kernel(const NormFw
     ss = sum_sq(f[k], ss);
   }
   ss = row_sum(ss, buf);
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+  const float rstd = rstd_of(ss, p.cols, p.eps);
   if (live && threadIdx.x == 0 && p.rstd) p.rstd[r] = rstd;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(MAXT, MINB) add_rmsnorm_quant_ring_kernel(cons
     }
     ss = ring_sum(ss, bars.red[it & 1]);
     if (threadIdx.x == 0) copy_in(it + stages);
-    float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+    float rstd = rstd_of(ss, p.cols, p.eps);
     if (!ok) rstd = __uint_as_float(0x7FFFFFFFu);  // a copy that never arrived shows as NaN
     if (threadIdx.x == 0 && p.rstd) p.rstd[r] = rstd;
 #pragma unroll
