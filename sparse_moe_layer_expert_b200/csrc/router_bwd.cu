@@ -353,7 +353,9 @@ __device__ __forceinline__ void quad_transpose(float (&f)[8], int lane) {
   }
 }
 
-// dx += v, one FP32 addition per element
+// dx += v, one FP32 addition per element, in the L2 (T = 4096, H = 7168: dx added
+// to 76 us, overwritten 41; reading dx a block or a unit ahead and storing the sums
+// took 88 and 116).
 __device__ __forceinline__ void red_add_v4(float *p, const float4 &v) {
   asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
                "f"(v.w)
