@@ -639,7 +639,8 @@ MOE_API int moe_block_forward(const moe_config *cfg, const moe_weights *w, const
  *   h_dev, y_dev, rstd_dev  the forward's (h_dev: its x_dev without resid)
  *   dout_dev   bf16 [T, H]
  *   balance    nullable (see moe_router_backward)
- *   dx_dev     dx_dtype [T, H]: the gradient of x, and of resid
+ *   dx_dev     dx_dtype [T, H]: the gradient of x, and of resid; in bf16 it may be
+ *              dout_dev, h_dev or y_dev
  *   dnorm_dev  float [H], nullable;  dwr_dev float [N_r, H]
  *   dW13_dev, dW2_dev, w13t_dev .. s2t_dev, fwd_ws_dev  as moe_backward's
  *   ws_dev     moe_block_backward_workspace_size() bytes, 256-byte aligned;

@@ -1370,6 +1370,8 @@ int moe_block_backward(const moe_config *cfg, const moe_weights *w, const uint8_
       !aligned16(w->wr_dev) || !aligned16(w13t) || !aligned16(w2t) || !aligned4(s13t) || !aligned4(s2t) ||
       !aligned4(err_flag) || (reinterpret_cast<uintptr_t>(ws) & 255) || (reinterpret_cast<uintptr_t>(fwd_ws) & 255))
     return MOE_ERR_INVALID_ARG;
+  // dx may take the place of dout, h or y, element for element
+  if (dx_dtype == MOE_DTYPE_F32 && (dx == dout || dx == h || dx == y)) return MOE_ERR_INVALID_ARG;
   moe_ws_layout F;
   make_layout(cfg, T, &F);
   if (fwd_ws_bytes < F.total) return MOE_ERR_WORKSPACE_TOO_SMALL;

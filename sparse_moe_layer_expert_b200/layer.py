@@ -120,11 +120,19 @@ class MoeLayer:
         of that size routed (routing held fixed): (dx, dW13, dW2) in FP32.
         The transposed weight copies the dgrad GEMMs read are made on first
         use (set-up) and kept."""
-        if getattr(self, "_wt", None) is None:
-            self._wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
+        wt = self._transposed(stream)
         T = x.shape[0]
-        return B.moe_backward(self.cfg, self.weights(), self._wt, x, dout, self.workspace(T),
+        return B.moe_backward(self.cfg, self.weights(), wt, x, dout, self.workspace(T),
                               ws=self.backward_workspace(T), err=self.err, stream=stream)
+
+    def _transposed(self, stream) -> dict:
+        wt = getattr(self, "_wt", None)
+        if wt is None:
+            wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
+            # copies made while a graph is captured are filled when it is replayed: that graph's own
+            if not torch.cuda.is_current_stream_capturing():
+                self._wt = wt
+        return wt
 
     def backward_workspace(self, T: int) -> torch.Tensor:
         bws = getattr(self, "_bws", None)
@@ -170,10 +178,9 @@ class MoeLayer:
     def block_backward(self, saved: dict, dout: torch.Tensor, balance=None, dx_dtype=None, stream=None) -> dict:
         """Gradients of block_forward's batch: dict(dx (of x and of resid),
         dnorm, dwr, dW13, dW2)."""
-        if getattr(self, "_wt", None) is None:
-            self._wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
+        wt = self._transposed(stream)
         T = dout.shape[0]
-        g = B.moe_block_backward(self.cfg, self.weights(), self._wt, saved["h"], saved["y"], saved["rstd"], dout,
+        g = B.moe_block_backward(self.cfg, self.weights(), wt, saved["h"], saved["y"], saved["rstd"], dout,
                                  self.workspace(T), norm_weight=saved["norm_weight"], balance=balance,
                                  dx_dtype=dx_dtype, ws=self.block_backward_workspace(T), err=self.err, stream=stream)
         return dict(zip(("dx", "dnorm", "dwr", "dW13", "dW2"), g))

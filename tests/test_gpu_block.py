@@ -213,3 +213,30 @@ def test_gate_gradient_against_the_unquantized_block(m):
     got = terms.sum(1)[pos]
     # terms of the double sum over I and H: |h| |W2| |dout|; their l2 size bounds what independent roundings do
     assert np.linalg.norm(got - want) <= 2.0 ** -3 * np.linalg.norm(want)
+
+
+def test_block_backward_captured_first_and_in_place(m):
+    """A layer's first backward under capture, then an eager one before any replay: the transposed weights of the
+    captured call are not there yet.  And bf16 dx in dout's, h's and y's place."""
+    T = 96
+    cfg, layer, x, resid, w, dout = problem(m, T, 11)
+    out, saved = layer.block_forward(x, resid, w, EPS)
+    layer.block_backward_workspace(T)
+    torch.cuda.synchronize()
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        got = layer.block_backward(saved, dout)
+    want = {k: v.clone() for k, v in layer.block_backward(saved, dout).items()}
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    fresh = problem(m, T, 11)[1]
+    fresh.block_forward(x, resid, w, EPS)
+    ref = fresh.block_backward(saved, dout)
+    assert all(torch.equal(ref[k], want[k]) for k in want)
+    for name in ("dout", "h", "y"):
+        a = dict(h=saved["h"].clone(), y=saved["y"].clone(), dout=dout.clone())
+        r = m.moe_block_backward(layer.cfg, layer.weights(), layer._wt, a["h"], a["y"], saved["rstd"], a["dout"],
+                                 layer.workspace(T), norm_weight=w, dx=a[name], err=layer.err)
+        assert r[0] is a[name] and torch.equal(r[0], want["dx"]), name
+    layer.check()

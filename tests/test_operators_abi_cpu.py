@@ -157,3 +157,20 @@ def test_block_refusals(m):
                 dict(dW13=None), dict(f=None), dict(ws=128), dict(err=None), dict(dxt=2), dict(dx=24), dict(nw=20),
                 dict(bal=C.byref(bal))):
         assert bwd(**bad) == m.MOE_ERR_INVALID_ARG, bad
+
+
+def test_block_backward_in_place_refusals(m):
+    """dx may take the place of dout, h or y in bf16 alone: FP32 rows are wider."""
+    cfg = m.config(512, 256, 16, 4)
+    w = m._binding.MoeWeights(16, 16, 16, 16, 16)
+    need = m.moe_workspace_size(cfg, 64)
+    need_b = m.lib.moe_block_backward_workspace_size(C.byref(cfg), 64)
+
+    def bwd(dx, dxt):
+        h, y, dout = 32, 48, 64
+        return m.lib.moe_block_backward(C.byref(cfg), C.byref(w), 16, 16, 16, 16, None, h, y, 16, dout, 64, None, dx,
+                                        dxt, None, 16, 16, 16, 256, need, 256, need_b, 16, None)
+
+    for dx in (32, 48, 64):
+        assert bwd(dx, 1) == m.MOE_ERR_INVALID_ARG and bwd(dx, 0) == m.MOE_ERR_NO_DEVICE
+    assert bwd(80, 1) == m.MOE_ERR_NO_DEVICE
