@@ -174,19 +174,44 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
   return s;
 }
 
-// Codes of 8 values of a tile with scale S.  y carries FP32 rounding already,
-// so y times the reciprocal of S (one Newton step on the hardware's: 2
-// roundings in all) serves for the quotient; a tiny S, whose reciprocal
-// overflows, takes the division, and a NaN one gives NaN codes.
+// a <- -(a / S), the IEEE quotient as div_by_recip forms it, two values an
+// instruction; ny = -RN(1 / S).  With the quotient negated throughout, the
+// residual step keeps the sign of a zero without a copysign: a = -0 gives
+// residual +0 and (+0) ny + (+0) = +0, the negative of -0.
+__device__ __forceinline__ void neg_quot2(float &a0, float &a1, float S, float ny) {
+  uint64_t a, q, r, s2, n2;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(S));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(n2) : "f"(ny));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(a), "l"(n2));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(s2), "l"(q), "l"(a));  // what the quotient leaves of a
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(n2), "l"(q));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(q));
+}
+
+// Codes of 8 values of a tile with scale S: those of the correctly rounded
+// quotients y / S, as in quant.cu.  A power of two scales exactly, so one
+// product serves there; a tiny S, whose reciprocal overflows, takes the
+// division, and a NaN one gives NaN codes.  (y times the reciprocal alone moved
+// one code in a few million by a step; the two operations more are hidden
+// behind the memory traffic.)
+template <bool POW2>
 __device__ __forceinline__ uint2 tile_codes(float (&f)[8], float S) {
   uint32_t lo = 0, hi = 0;
   if (S >= 0x1p-100f) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(S));
-    r = fmaf(fmaf(-S, r, 1.0f), r, r);
-    mul8(f, r);
+    const float r = __frcp_rn(S);
+    if (POW2) {
+      mul8(f, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) neg_quot2(f[i], f[i + 1], S, -r);
+    }
     lo = e4m3x2_rn_sat(f[0], f[1]) | (e4m3x2_rn_sat(f[2], f[3]) << 16);
     hi = e4m3x2_rn_sat(f[4], f[5]) | (e4m3x2_rn_sat(f[6], f[7]) << 16);
+    if (!POW2) {
+      lo ^= 0x80808080u;
+      hi ^= 0x80808080u;
+    }
   } else if (S != 0.0f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) lo |= static_cast<uint32_t>(e4m3_rn_sat(f[i] / S)) << (8 * i);
@@ -236,7 +261,7 @@ __device__ __forceinline__ void finish_chunk(float (&f)[8], const float (&w)[8],
   }
   const float S = tile_scale<POW2>(am);
   if (in) {
-    *reinterpret_cast<uint2 *>(q) = tile_codes(f, S);
+    *reinterpret_cast<uint2 *>(q) = tile_codes<POW2>(f, S);
     if ((threadIdx.x & 15) == 0) *s = S;
   }
 }
