@@ -328,8 +328,9 @@ MOE_API int moe_profile_events(void *const *events, int32_t n_events);
  * The gates' own gradient is not part of this (moe_router_backward,
  * moe_block_backward).
  *
- * moe_transpose_weights (set-up): the dgrad GEMMs' weights, each expert's
- * codes and 128x128 block scales transposed:
+ * moe_transpose_weights (set-up, and again whenever the weights change): the
+ * dgrad GEMMs' weights, each expert's codes and 128x128 block scales
+ * transposed:
  *   w13t_dev E4M3 [E, H, 2I], s13t_dev float [E, H/128, 2I/128]
  *   w2t_dev  E4M3 [E, I, H],  s2t_dev  float [E, I/128, H/128]
  * moe_backward: call after the moe_forward of the same batch, same cfg and T,

@@ -384,16 +384,18 @@ def moe_ep_combine(cfg: MoeConfig, world: int, x, row_of, back, y_shared, out, o
 
 
 # ------------------------------------------------------------ backward
-def moe_transpose_weights(cfg: MoeConfig, w: dict, stream=None) -> dict:
+def moe_transpose_weights(cfg: MoeConfig, w: dict, stream=None, out=None) -> dict:
     """The dgrad GEMMs' weights: each expert's codes and block scales
-    transposed (w13t [E, H, 2I], s13t, w2t [E, I, H], s2t)."""
+    transposed (w13t [E, H, 2I], s13t, w2t [E, I, H], s2t), into `out` if
+    given.  To be called again when the weights change."""
     E, I2, H = w["w13"].shape
     I = I2 // 2
     dev = w["w13"].device
-    t = dict(w13t=torch.empty((E, H, I2), dtype=torch.uint8, device=dev),
-             s13t=torch.empty((E, H // 128, I2 // 128), dtype=torch.float32, device=dev),
-             w2t=torch.empty((E, I, H), dtype=torch.uint8, device=dev),
-             s2t=torch.empty((E, I // 128, H // 128), dtype=torch.float32, device=dev))
+    t = out if out is not None else dict(
+        w13t=torch.empty((E, H, I2), dtype=torch.uint8, device=dev),
+        s13t=torch.empty((E, H // 128, I2 // 128), dtype=torch.float32, device=dev),
+        w2t=torch.empty((E, I, H), dtype=torch.uint8, device=dev),
+        s2t=torch.empty((E, I // 128, H // 128), dtype=torch.float32, device=dev))
     ws = weights_struct(w)
     _check(lib.moe_transpose_weights(C.byref(cfg), C.byref(ws), _ptr(t["w13t"]), _ptr(t["s13t"]), _ptr(t["w2t"]),
                                      _ptr(t["s2t"]), _stream(stream)), "moe_transpose_weights")

@@ -30,14 +30,30 @@ class MoeLayer:
         self.bias = torch.zeros((c.n_routed,), dtype=torch.float32, device=dev)
         self.err = B.new_err_flag(dev)
         self._ws: dict[int, torch.Tensor] = {}
+        self._copies: dict = {}
 
     # -------------------------------------------------------------- weights
     def set_expert(self, e: int, w13_bf16: torch.Tensor, w2_bf16: torch.Tensor, stream=None) -> None:
         """Quantize expert e's bf16 weights (128x128 blocks) into place, with
-        the scale rule of the layer's scale mode."""
+        the scale rule of the layer's scale mode.  The transposed copies that
+        the backward reads, where they exist, follow in the same call."""
         pow2 = self.cfg.scale_mode == B.MOE_SCALE_POW2
         B.fp8_quant_128x128(w13_bf16.contiguous(), q=self.w13[e], scales=self.s13[e], stream=stream, pow2=pow2)
         B.fp8_quant_128x128(w2_bf16.contiguous(), q=self.w2[e], scales=self.s2[e], stream=stream, pow2=pow2)
+        wt = self._wt
+        if wt is not None:
+            one = slice(e, e + 1)
+            B.moe_transpose_weights(B.config(self.cfg.hidden, self.cfg.inter, 1, 1, 0),
+                                    {k: t if k == "wr" else t[one] for k, t in self.weights().items()},
+                                    out={k: t[one] for k, t in wt.items()}, stream=stream)
+
+    def weights_changed(self, stream=None) -> None:
+        """To be called after w13, s13, w2 or s2 were written in place other
+        than by set_expert of this layer or a sibling: brings the transposed
+        copies that the backward reads, where they exist, up to date."""
+        wt = self._wt
+        if wt is not None:
+            B.moe_transpose_weights(self.cfg, self.weights(), out=wt, stream=stream)
 
     def set_router(self, wr_bf16: torch.Tensor, bias: torch.Tensor) -> None:
         self.wr.copy_(wr_bf16)
@@ -67,6 +83,7 @@ class MoeLayer:
         other.bias = self.bias.clone() if bias is None else bias
         other.err = B.new_err_flag(self.device)
         other._ws = {}
+        other._copies = self._copies
         return other
 
     def weights(self) -> dict:
@@ -119,19 +136,35 @@ class MoeLayer:
         """Gradients of the expert FFNs for the batch this layer's last forward
         of that size routed (routing held fixed): (dx, dW13, dW2) in FP32.
         The transposed weight copies the dgrad GEMMs read are made on first
-        use (set-up) and kept."""
+        use and kept; set_expert and weights_changed bring them up to date."""
         wt = self._transposed(stream)
         T = x.shape[0]
         return B.moe_backward(self.cfg, self.weights(), wt, x, dout, self.workspace(T),
                               ws=self.backward_workspace(T), err=self.err, stream=stream)
 
+    # Transposed copies of the weights: one set for all siblings, in the same
+    # memory from then on, so that a captured backward reads the weights as they
+    # are when it is replayed.
+    def _weight_tensors(self) -> tuple:
+        return self.w13, self.s13, self.w2, self.s2
+
+    @property
+    def _wt(self) -> dict | None:
+        c = self._copies
+        # other tensors in the weights' places: the copies are not theirs
+        if c and all(a is b for a, b in zip(c["of"], self._weight_tensors())):
+            return c["wt"]
+        return None
+
     def _transposed(self, stream) -> dict:
-        wt = getattr(self, "_wt", None)
+        wt = self._wt
         if wt is None:
             wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
             # copies made while a graph is captured are filled when it is replayed: that graph's own
             if not torch.cuda.is_current_stream_capturing():
-                self._wt = wt
+                if self._copies:
+                    self._copies = {}
+                self._copies.update(of=self._weight_tensors(), wt=wt)
         return wt
 
     def backward_workspace(self, T: int) -> torch.Tensor:
@@ -177,7 +210,8 @@ class MoeLayer:
 
     def block_backward(self, saved: dict, dout: torch.Tensor, balance=None, dx_dtype=None, stream=None) -> dict:
         """Gradients of block_forward's batch: dict(dx (of x and of resid),
-        dnorm, dwr, dW13, dW2)."""
+        dnorm, dwr, dW13, dW2).  The weights are those of now: change them
+        with set_expert, or call weights_changed."""
         wt = self._transposed(stream)
         T = dout.shape[0]
         g = B.moe_block_backward(self.cfg, self.weights(), wt, saved["h"], saved["y"], saved["rstd"], dout,
