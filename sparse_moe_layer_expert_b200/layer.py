@@ -6,6 +6,8 @@ grouped GEMMs and the combine all run in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _binding as B
@@ -112,6 +114,22 @@ class MoeLayer:
             self._ws[T] = ws
         return ws
 
+    # What a call allocates belongs to the stream it runs on; what it finds is
+    # made known to the allocator as used there too, so that neither is given
+    # away while that stream still works with it.
+    def _on(self, stream):
+        return contextlib.nullcontext() if stream is None else B._use_stream(stream, self.bias)
+
+    def _used(self, t: torch.Tensor, stream=None) -> torch.Tensor:
+        handle = torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else B._stream(stream)
+        seen = t.__dict__.setdefault("on_streams", set())
+        if handle not in seen:
+            with self._on(stream):
+                if not torch.cuda.is_current_stream_capturing():  # (a capture's memory has to outlive its graph anyway)
+                    t.record_stream(torch.cuda.current_stream(t.device))
+                    seen.add(handle)
+        return t
+
     def check_guards(self) -> None:
         """Raise if any guard band around this layer's workspaces changed."""
         for buf, g, n in getattr(self, "_guarded", []):
@@ -121,8 +139,13 @@ class MoeLayer:
 
     def forward(self, x: torch.Tensor, out=None, out_dtype=B.MOE_DTYPE_BF16, idx_out=None, counts_out=None,
                 stream=None) -> torch.Tensor:
+        T = x.shape[0]
+        if stream is not None and (out is None or T not in self._ws):  # something is allocated
+            with self._on(stream):
+                return self.forward(x, out, out_dtype, idx_out, counts_out)
         return B.moe_forward(self.cfg, self.weights(), self.bias, x, out=out, out_dtype=out_dtype, idx_out=idx_out,
-                             counts_out=counts_out, ws=self.workspace(x.shape[0]), err=self.err, stream=stream)
+                             counts_out=counts_out, ws=self._used(self.workspace(T), stream), err=self.err,
+                             stream=stream)
 
     def bias_update(self, counts: torch.Tensor, T: int, gamma: float = 0.001, stream=None) -> None:
         B.moe_bias_update(self.bias, counts, self.cfg.n_routed, T * self.cfg.top_k, gamma, stream=stream)
@@ -137,10 +160,10 @@ class MoeLayer:
         of that size routed (routing held fixed): (dx, dW13, dW2) in FP32.
         The transposed weight copies the dgrad GEMMs read are made on first
         use and kept; set_expert and weights_changed bring them up to date."""
-        wt = self._transposed(stream)
         T = x.shape[0]
-        return B.moe_backward(self.cfg, self.weights(), wt, x, dout, self.workspace(T),
-                              ws=self.backward_workspace(T), err=self.err, stream=stream)
+        with self._on(stream):
+            return B.moe_backward(self.cfg, self.weights(), self._transposed(), x, dout, self._used(self.workspace(T)),
+                                  ws=self._used(self.backward_workspace(T)), err=self.err)
 
     # Transposed copies of the weights: one set for all siblings, in the same
     # memory from then on, so that a captured backward reads the weights as they
@@ -156,15 +179,23 @@ class MoeLayer:
             return c["wt"]
         return None
 
-    def _transposed(self, stream) -> dict:
+    def _transposed(self) -> dict:
+        """The copies, made now if there are none, for the current stream."""
+        cur = torch.cuda.current_stream(self.device)
+        capturing = torch.cuda.is_current_stream_capturing()
         wt = self._wt
         if wt is None:
-            wt = B.moe_transpose_weights(self.cfg, self.weights(), stream=stream)
+            wt = B.moe_transpose_weights(self.cfg, self.weights())
             # copies made while a graph is captured are filled when it is replayed: that graph's own
-            if not torch.cuda.is_current_stream_capturing():
+            if not capturing:
                 if self._copies:
                     self._copies = {}
-                self._copies.update(of=self._weight_tensors(), wt=wt)
+                self._copies.update(of=self._weight_tensors(), wt=wt, filled=cur.record_event(), on=cur)
+        elif cur != self._copies["on"] and not capturing:
+            # (a capture cannot wait for what runs outside it; torch.cuda.graph waits for the device first)
+            cur.wait_event(self._copies["filled"])
+        for t in wt.values():
+            self._used(t)
         return wt
 
     def backward_workspace(self, T: int) -> torch.Tensor:
@@ -185,10 +216,11 @@ class MoeLayer:
         saved).  `saved` is what block_backward takes; the routing and the
         experts' state stay in this layer's workspace for that batch size, so
         the backward has to come before its next forward of the same size."""
-        T = x.shape[0]
-        out, h, y, rstd = B.moe_block_forward(self.cfg, self.weights(), self.bias, x, resid, norm_weight, eps, out=out,
-                                              out_dtype=out_dtype, idx_out=idx_out, counts_out=counts_out,
-                                              ws=self.workspace(T), err=self.err, stream=stream)
+        with self._on(stream):
+            out, h, y, rstd = B.moe_block_forward(self.cfg, self.weights(), self.bias, x, resid, norm_weight, eps,
+                                                  out=out, out_dtype=out_dtype, idx_out=idx_out,
+                                                  counts_out=counts_out, ws=self._used(self.workspace(x.shape[0])),
+                                                  err=self.err)
         return out, dict(h=h, y=y, rstd=rstd, norm_weight=norm_weight)
 
     def router_state(self, T: int):
@@ -205,18 +237,21 @@ class MoeLayer:
         batch this layer's last forward of T tokens routed: (loss, grad), grad
         being what block_backward takes as `balance` (dloss: ones)."""
         logits, idx = self.router_state(T)
-        loss, counts = B.moe_balance_loss(self.cfg, logits, idx, seq_offsets, alpha=alpha, err=self.err, stream=stream)
+        with self._on(stream):
+            self._used(self.workspace(T))
+            loss, counts = B.moe_balance_loss(self.cfg, logits, idx, seq_offsets, alpha=alpha, err=self.err)
         return loss, dict(seq_offsets=seq_offsets, counts=counts, alpha=alpha)
 
     def block_backward(self, saved: dict, dout: torch.Tensor, balance=None, dx_dtype=None, stream=None) -> dict:
         """Gradients of block_forward's batch: dict(dx (of x and of resid),
         dnorm, dwr, dW13, dW2).  The weights are those of now: change them
         with set_expert, or call weights_changed."""
-        wt = self._transposed(stream)
         T = dout.shape[0]
-        g = B.moe_block_backward(self.cfg, self.weights(), wt, saved["h"], saved["y"], saved["rstd"], dout,
-                                 self.workspace(T), norm_weight=saved["norm_weight"], balance=balance,
-                                 dx_dtype=dx_dtype, ws=self.block_backward_workspace(T), err=self.err, stream=stream)
+        with self._on(stream):
+            g = B.moe_block_backward(self.cfg, self.weights(), self._transposed(), saved["h"], saved["y"],
+                                     saved["rstd"], dout, self._used(self.workspace(T)),
+                                     norm_weight=saved["norm_weight"], balance=balance, dx_dtype=dx_dtype,
+                                     ws=self._used(self.block_backward_workspace(T)), err=self.err)
         return dict(zip(("dx", "dnorm", "dwr", "dW13", "dW2"), g))
 
     def block_backward_workspace(self, T: int) -> torch.Tensor:
