@@ -1177,12 +1177,11 @@ cudaError_t run_router_bwd(const moe_config *cfg, moe::RouterBwd g, const void *
   make_router_bwd_layout(cfg, g.T, &L);
   g.parts = dx || dwr ? at<void *>(ws, L.parts) : nullptr;
   cudaError_t e = moe::launch_router_dz(g, st);
-  if (e == cudaSuccess && dx)
-    e = moe::launch_router_dx(g.parts, wr, g.T, g.Nr, cfg->hidden, dx, accumulate, dwr != nullptr, g.err,
-                              moe::kDefaultWaitLimitNs, st);
-  if (e == cudaSuccess && dwr)
-    e = moe::launch_router_dwr(g.parts, x, g.T, g.Nr, cfg->hidden, at<float *>(ws, L.dwr), dwr, dx != nullptr,
-                               g.err, moe::kDefaultWaitLimitNs, st);
+  if (e == cudaSuccess && (dx || dwr)) {
+    const moe::RouterProducts p{g.parts,           g.T,   g.Nr,  cfg->hidden, wr, dx, accumulate, x,
+                                at<float *>(ws, L.dwr), dwr, g.err, moe::kDefaultWaitLimitNs};
+    e = moe::launch_router_products(p, st);
+  }
   return e;
 }
 }  // namespace

@@ -264,14 +264,22 @@ struct RouterBwd {
   int32_t *err;
 };
 int router_parts_pitch(int Nr);
-size_t router_dwr_scratch(int64_t T, int cols);  // bytes of launch_router_dwr's part
+size_t router_dwr_scratch(int64_t T, int cols);  // bytes of RouterProducts::part
 cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st);
-// beside_dwr: launch_router_dwr comes directly behind it and shares the SMs
-cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
-                             bool beside_dwr, int32_t *err, uint64_t limit_ns, cudaStream_t st);
-// behind_dx: launch_router_dx came directly before it on the stream (else launch_router_dz)
-cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
-                              bool behind_dx, int32_t *err, uint64_t limit_ns, cudaStream_t st);
+struct RouterProducts {
+  const void *parts;  // launch_router_dz's, directly before on the stream
+  int64_t T;
+  int Nr, H;
+  const void *wr;     // bf16 [Nr, H]
+  float *dx;          // [T, H] or null
+  int accumulate;     // add to dx
+  const void *x;      // bf16 [T, H]
+  float *part;        // scratch
+  float *dwr;         // [Nr, H] or null
+  int32_t *err;
+  uint64_t limit_ns;
+};
+cudaError_t launch_router_products(const RouterProducts &g, cudaStream_t st);
 
 // weight-block pairs (tiles) per chunk of activations in each grouped GEMM
 __host__ __device__ inline int gemm1_blocks(int I) { return I / 128; }

@@ -26,10 +26,11 @@
 //                      (K-major), B = W_r as it lies (N-major)
 //   router_dwr_kernel  all experts x 256 columns of x per pair of CTAs over a
 //                      range of tokens, so x is read once; both operands
-//                      M/N-major (tokens are the slow index of both).  It needs
-//                      dz alone and starts on the SMs that router_dx_kernel
-//                      leaves
+//                      M/N-major (tokens are the slow index of both)
+//   router_dx_dwr_kernel  both products at once, pairs of CTAs for each
 //   dwr_join_kernel    adds the token ranges' partial sums in range order
+// Each is launched by launch_next behind the one before it and reads what that
+// one or an earlier one wrote only behind predecessor_done.
 #include "common.cuh"
 #include "kernels.h"
 #include "operators.cuh"
@@ -363,9 +364,9 @@ __device__ __forceinline__ void red_add_v4(float *p, const float4 &v) {
 }
 }  // namespace
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
-    router_dx_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                     const DxArgs args) {
+// Pair `pair` of `pairs`.  The CTA may have more warps than X_THREADS.
+__device__ __forceinline__ void dx_pair(const CUtensorMap &map_a, const CUtensorMap &map_w, const DxArgs &args,
+                                        int pair, int pairs) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sa = smem, *sb = sa + X_A;
@@ -401,12 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   const uint32_t tmem = bars->tmem_base;
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
-  const PairUnits pu = pair_units(blockIdx.x >> 1, gridDim.x >> 1, args.n_strips * args.m_tiles);
+  const PairUnits pu = pair_units(pair, pairs, args.n_strips * args.m_tiles);
   const int nk = args.kb * X_KPB;  // stages per unit
-  // in this order: what starts behind this kernel (router_dwr_kernel) relies on
-  // dz being complete by then
-  predecessor_done();
   dependents_start();
+  predecessor_done();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -489,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
       umma_commit_pair(&bars->teardown, 0x1);
       mbar_wait(&bars->teardown, 0, drain);
     }
-  } else {
+  } else if (warp < X_THREADS / 32) {
     const int q = warp & 3;           // TMEM lane quarter
     const int half = (warp - 2) >> 2;  // column half
     const bool wide = (reinterpret_cast<uintptr_t>(args.dx) & 31) == 0;
@@ -550,9 +549,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(X_THREADS, 1)
+    router_dx_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                     const DxArgs args) {
+  dx_pair(map_a, map_w, args, blockIdx.x >> 1, gridDim.x >> 1);
+}
+
 // ------------------------------------------------------------ dW_r = dz^T x
 // Units (256-column strip of x, 64-token stage), strip-major, in as many equal runs
-// as the device has pairs; a pair takes one run, or where router_dx_kernel has
+// as the device has pairs; a pair takes one run, or where dx's pairs have
 // the other half of the SMs, two.  A strip's tokens are so shared out over several
 // runs and every SM has the same work.  The tensor core's FP32 accumulation drops the bits
 // below its 24 at every step (measured: the error grows with the number of
@@ -587,7 +592,6 @@ struct DwrArgs {
   int Nr;
   int n_runs;              // what the units are shared out to
   float *part;             // [n_runs + n_strips, 256, 256]
-  int behind_dx;           // launched behind router_dx_kernel, not router_dz_kernel
   int32_t *err;
   uint64_t limit_ns;
 };
@@ -603,9 +607,9 @@ struct DwrBars {
 static_assert(sizeof(DwrBars) <= 256, "barrier block");
 }  // namespace
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
-    router_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
-                      const DwrArgs args) {
+// Pair `pair` of `pairs` (WR_THREADS threads a CTA, launched with 168 registers each).
+__device__ __forceinline__ void dwr_pair(const CUtensorMap &map_a, const CUtensorMap &map_x, const DwrArgs &args,
+                                         int pair, int pairs) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DwrBars *bars = reinterpret_cast<DwrBars *>(smem + WR_STAGES * WR_STAGE);
@@ -637,11 +641,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   volatile int *abortp = &bars->abort_flag;
   const WaitCtl ctl{abortp, args.err, args.limit_ns};
   // this pair's share [r0, r1) of the runs that the units fall into
-  const PairUnits runs = pair_units(blockIdx.x >> 1, gridDim.x >> 1, args.n_runs);
+  const PairUnits runs = pair_units(pair, pairs, args.n_runs);
   const int units = args.n_strips * args.n_stages;
 
   dependents_start();
-  if (!args.behind_dx) predecessor_done();
+  predecessor_done();
 
   // Register split as in gemm_pair.cu: 128 * 72 + 256 * 216 = 384 * 168
   if (warp < 4) {
@@ -787,8 +791,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
-  // what follows this kernel on the stream comes behind router_dx_kernel too
-  if (args.behind_dx) predecessor_done();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
+    router_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                      const DwrArgs args) {
+  dwr_pair(map_a, map_x, args, blockIdx.x >> 1, gridDim.x >> 1);
+}
+
+// Both products side by side, the first dx_pairs pairs on dx.  One launch, so
+// that both start behind router_dz_kernel by the same predecessor_done (dW_r as a
+// launch of its own would have to wait for dx, or read dz without waiting).
+constexpr int BOTH_SMEM = X_SMEM > WR_SMEM ? X_SMEM : WR_SMEM;
+static_assert(X_THREADS <= WR_THREADS, "dx's warps");
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
+    router_dx_dwr_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                         const DxArgs dx, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ CUtensorMap map_x, const DwrArgs dwr, int dx_pairs) {
+  const int pair = blockIdx.x >> 1;
+  if (pair < dx_pairs)
+    dx_pair(map_a, map_w, dx, pair, dx_pairs);
+  else
+    dwr_pair(map_b, map_x, dwr, pair - dx_pairs, (gridDim.x >> 1) - dx_pairs);
 }
 
 // dW_r [Nr, cols] from the pieces of each strip, in token order.  CTA (4
@@ -848,8 +872,8 @@ int dwr_pairs(int64_t T, int cols) {
 // Whether dx and dW_r, both asked for, run side by side on half of the SMs each:
 // dx alone is held up by its stores and dW_r by its loads, but with many units a
 // pair both reach the matrix rate by themselves.  (H = 7168, N_r = 256, a pass:
-// T = 512 32.4 us one after the other, 30.7 side by side; 2048 53.6, 49.3; 4096
-// 78.7, 77.3; 8192 139, 141; 16381 265, 273.)
+// T = 512 34.7 us one after the other, 27.1 side by side; 2048 55.4, 47.2; 4096
+// 80.1, 77.2; 8192 150.5, 151.3; 16381 294, 301.)
 static bool share_sms(int64_t T, int cols) {
   return static_cast<int64_t>(strips_of(cols)) * ((T + 255) / 256) < 12 * most_pairs();
 }
@@ -892,79 +916,86 @@ cudaError_t launch_router_dz(const RouterBwd &g, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_router_dx(const void *parts, const void *wr, int64_t T, int Nr, int H, float *dx, int accumulate,
-                             bool beside_dwr, int32_t *err, uint64_t limit_ns, cudaStream_t st) {
-  if (T == 0) return cudaSuccess;
-  const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
-  // in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], W_r [H / 64][Nr][64]
-  const uint64_t da[4] = {64, t, Np / 64, kParts}, sa[3] = {Np * 2, 128, t * Np * 2};
-  const uint64_t dw[3] = {64, static_cast<uint64_t>(Nr), h / 64}, sw[2] = {h * 2, 128};
-  const uint32_t ba[4] = {64, 128, 1, kParts}, bw[3] = {64, X_K, 2};
-  CUtensorMap ma, mw;
-  if (moe_host::encode_tmap(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, 4, da, sa, ba) != 0 ||
-      moe_host::encode_tmap(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wr, 3, dw, sw, bw) != 0)
-    return cudaErrorInvalidValue;
+// dx = dz W_r and dW_r = dz^T x, those asked for, behind launch_router_dz.
+cudaError_t launch_router_products(const RouterProducts &g, cudaStream_t st) {
+  if (g.T == 0)
+    return g.dwr ? cudaMemsetAsync(g.dwr, 0, sizeof(float) * g.Nr * static_cast<size_t>(g.H), st) : cudaSuccess;
+  const uint64_t Np = router_parts_pitch(g.Nr), t = g.T, h = g.H;
+  // every operand in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], W_r [H / 64][Nr][64],
+  // x [H / 64][T][64]
+  const uint64_t dp[4] = {64, t, Np / 64, kParts}, sp[3] = {Np * 2, 128, t * Np * 2};
+  const auto BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  static std::atomic<int> resident[3][64];
   DxArgs a{};
-  a.T = T;
-  a.cols = H;
-  a.n_strips = strips_of(H);
-  a.m_tiles = static_cast<int>((T + 255) / 256);
-  a.kb = static_cast<int>(Np / 64);
-  a.dx = dx;
-  a.accumulate = accumulate;
-  a.err = err;
-  a.limit_ns = limit_ns;
-  static std::atomic<uint64_t> attr_done{0};
-  if (const cudaError_t e = smem_attr_once(router_dx_kernel, X_SMEM, attr_done)) return e;
-  const int units = a.n_strips * a.m_tiles;
-  static std::atomic<int> resident[64];
-  int64_t pairs = resident_pairs(router_dx_kernel, X_THREADS, X_SMEM, most_pairs(), resident);
-  if (beside_dwr && share_sms(T, H)) pairs = (pairs + 1) / 2;
-  if (pairs > units) pairs = units;
-  if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  return launch_next(router_dx_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(X_THREADS), X_SMEM, st, ma, mw, a);
-}
-
-cudaError_t launch_router_dwr(const void *parts, const void *x, int64_t T, int Nr, int H, float *part, float *dwr,
-                              bool behind_dx, int32_t *err, uint64_t limit_ns, cudaStream_t st) {
-  if (T == 0) return cudaMemsetAsync(dwr, 0, sizeof(float) * Nr * static_cast<size_t>(H), st);
-  const uint64_t Np = router_parts_pitch(Nr), t = T, h = H;
-  DwrArgs a{};
-  a.T = T;
-  a.n_strips = strips_of(H);
-  a.n_stages = dwr_stages(T);
-  a.Nr = Nr;
-  a.part = part;
-  a.behind_dx = behind_dx;
-  a.err = err;
-  a.limit_ns = limit_ns;
-  // both operands in groups of 64 elements (128 bytes) of a row: parts [3][Np / 64][T][64], x [H / 64][T][64]
-  const uint64_t da[4] = {64, t, Np / 64, kParts}, sa[3] = {Np * 2, 128, t * Np * 2};
-  const uint64_t dx[3] = {64, t, h / 64}, sx[2] = {h * 2, 128};
-  const uint32_t ba[4] = {64, WR_TOK, 2, kParts}, bx[3] = {64, WR_TOK, 2};
-  CUtensorMap ma, mx;
-  if (moe_host::encode_tmap(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts, 4, da, sa, ba) != 0 ||
-      moe_host::encode_tmap(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dx, sx, bx) != 0)
-    return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> attr_done{0};
-  if (const cudaError_t e = smem_attr_once(router_dwr_kernel, WR_SMEM, attr_done)) return e;
-  static std::atomic<int> resident[64];
-  int64_t runs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident);
-  if (runs > dwr_pairs(T, H)) runs = dwr_pairs(T, H);
-  if (runs < 1) return cudaErrorLaunchOutOfResources;
-  a.n_runs = static_cast<int>(runs);
-  // beside dx, half of the pairs take two runs each, where the runs need them
-  int64_t pairs = runs;
-  if (behind_dx && share_sms(T, H)) {
-    const int64_t left = most_pairs() - (most_pairs() + 1) / 2;
-    if (pairs > left) pairs = (runs + 1) / 2;
+  CUtensorMap ma, mw;
+  int64_t pairs = 0;
+  if (g.dx) {
+    const uint64_t dw[3] = {64, static_cast<uint64_t>(g.Nr), h / 64}, sw[2] = {h * 2, 128};
+    const uint32_t ba[4] = {64, 128, 1, kParts}, bw[3] = {64, X_K, 2};
+    if (moe_host::encode_tmap(&ma, BF16, g.parts, 4, dp, sp, ba) != 0 ||
+        moe_host::encode_tmap(&mw, BF16, g.wr, 3, dw, sw, bw) != 0)
+      return cudaErrorInvalidValue;
+    a.T = g.T;
+    a.cols = g.H;
+    a.n_strips = strips_of(g.H);
+    a.m_tiles = static_cast<int>((g.T + 255) / 256);
+    a.kb = static_cast<int>(Np / 64);
+    a.dx = g.dx;
+    a.accumulate = g.accumulate;
+    a.err = g.err;
+    a.limit_ns = g.limit_ns;
+    static std::atomic<uint64_t> done{0};
+    if (const cudaError_t e = smem_attr_once(router_dx_kernel, X_SMEM, done)) return e;
+    pairs = resident_pairs(router_dx_kernel, X_THREADS, X_SMEM, most_pairs(), resident[0]);
   }
-  cudaError_t e = launch_next(router_dwr_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(WR_THREADS), WR_SMEM, st,
-                              ma, mx, a);
-  if (e != cudaSuccess) return e;
-  return launch_next(dwr_join_kernel, dim3(static_cast<unsigned>((Nr + 3) / 4), static_cast<unsigned>(a.n_strips)),
-                     dim3(256), 0, st, static_cast<const float *>(part), a.n_runs, a.n_strips, a.n_stages,
-                     Nr, H, dwr);
+  const int64_t units = static_cast<int64_t>(a.n_strips) * a.m_tiles;
+  DwrArgs b{};
+  CUtensorMap mb, mx;
+  if (g.dwr) {
+    const uint64_t dx[3] = {64, t, h / 64}, sx[2] = {h * 2, 128};
+    const uint32_t bb[4] = {64, WR_TOK, 2, kParts}, bx[3] = {64, WR_TOK, 2};
+    if (moe_host::encode_tmap(&mb, BF16, g.parts, 4, dp, sp, bb) != 0 ||
+        moe_host::encode_tmap(&mx, BF16, g.x, 3, dx, sx, bx) != 0)
+      return cudaErrorInvalidValue;
+    b.T = g.T;
+    b.n_strips = strips_of(g.H);
+    b.n_stages = dwr_stages(g.T);
+    b.Nr = g.Nr;
+    b.part = g.part;
+    b.err = g.err;
+    b.limit_ns = g.limit_ns;
+    static std::atomic<uint64_t> done{0};
+    if (const cudaError_t e = smem_attr_once(router_dwr_kernel, WR_SMEM, done)) return e;
+    // the runs, and so the sums' order, are the same with and without dx beside them
+    int64_t runs = resident_pairs(router_dwr_kernel, WR_THREADS, WR_SMEM, most_pairs(), resident[1]);
+    if (runs > dwr_pairs(g.T, g.H)) runs = dwr_pairs(g.T, g.H);
+    b.n_runs = static_cast<int>(runs);
+  }
+  if ((g.dx && pairs < 1) || (g.dwr && b.n_runs < 1)) return cudaErrorLaunchOutOfResources;
+
+  cudaError_t e = cudaSuccess;
+  if (g.dx && g.dwr && share_sms(g.T, g.H)) {
+    static std::atomic<uint64_t> done{0};
+    if ((e = smem_attr_once(router_dx_dwr_kernel, BOTH_SMEM, done)) != cudaSuccess) return e;
+    const int64_t all = resident_pairs(router_dx_dwr_kernel, WR_THREADS, BOTH_SMEM, most_pairs(), resident[2]);
+    int64_t p = (all + 1) / 2;
+    if (p > units) p = units;
+    // dW_r: a pair for each run where that many are left, else half as many
+    const int64_t q = b.n_runs <= all - p ? b.n_runs : (b.n_runs + 1) / 2;
+    e = launch_next(router_dx_dwr_kernel, dim3(static_cast<unsigned>(2 * (p + q))), dim3(WR_THREADS), BOTH_SMEM, st, ma,
+                    mw, a, mb, mx, b, static_cast<int>(p));
+  } else {
+    if (g.dx)
+      e = launch_next(router_dx_kernel, dim3(static_cast<unsigned>(2 * (pairs < units ? pairs : units))),
+                      dim3(X_THREADS), X_SMEM, st, ma, mw, a);
+    if (e == cudaSuccess && g.dwr)
+      e = launch_next(router_dwr_kernel, dim3(static_cast<unsigned>(2 * b.n_runs)), dim3(WR_THREADS), WR_SMEM, st, mb, mx,
+                      b);
+  }
+  if (e != cudaSuccess || !g.dwr) return e;
+  return launch_next(dwr_join_kernel, dim3(static_cast<unsigned>((g.Nr + 3) / 4), static_cast<unsigned>(b.n_strips)),
+                     dim3(256), 0, st, static_cast<const float *>(g.part), b.n_runs, b.n_strips, b.n_stages, g.Nr, g.H,
+                     g.dwr);
 }
 
 }  // namespace moe
