@@ -871,11 +871,16 @@ int dwr_pairs(int64_t T, int cols) {
 
 // Whether dx and dW_r, both asked for, run side by side on half of the SMs each:
 // dx alone is held up by its stores and dW_r by its loads, but with many units a
-// pair both reach the matrix rate by themselves.  (H = 7168, N_r = 256, a pass:
-// T = 512 34.7 us one after the other, 27.1 side by side; 2048 55.4, 47.2; 4096
-// 80.1, 77.2; 8192 150.5, 151.3; 16381 294, 301.)
-static bool share_sms(int64_t T, int cols) {
-  return static_cast<int64_t>(strips_of(cols)) * ((T + 255) / 256) < 12 * most_pairs();
+// pair both reach their own limit by themselves, the matrix rate or, with 64 experts
+// and fewer (a third of the matrix work or less beside the same memory traffic),
+// the memory's, which comes sooner.  (us a pass, one after the other / side by side,
+// H = 7168: N_r = 256, T = 512 34.7 / 27.1, 2048 55.4 / 47.2, 4096 80.1 / 77.2,
+// 8192 150.5 / 151.3, 16381 294 / 301; 128, 4096 69.7 / 68.6, 8192 125 / 127;
+// 64, 2048 44.3 / 40.9, 4096 63.7 / 65.7, 8192 106 / 119.  H = 2048, 64 experts:
+// 8192 49.8 / 47.9, 12288 65.4 / 64.8, 16381 77.6 / 82.0.)
+static bool share_sms(int64_t T, int cols, int Nr) {
+  const int64_t units = static_cast<int64_t>(strips_of(cols)) * ((T + 255) / 256);
+  return units < (Nr > 64 ? 12 : 5) * most_pairs();
 }
 
 size_t router_dwr_scratch(int64_t T, int cols) {
@@ -974,7 +979,7 @@ cudaError_t launch_router_products(const RouterProducts &g, cudaStream_t st) {
   if ((g.dx && pairs < 1) || (g.dwr && b.n_runs < 1)) return cudaErrorLaunchOutOfResources;
 
   cudaError_t e = cudaSuccess;
-  if (g.dx && g.dwr && share_sms(g.T, g.H)) {
+  if (g.dx && g.dwr && share_sms(g.T, g.H, g.Nr)) {
     static std::atomic<uint64_t> done{0};
     if ((e = smem_attr_once(router_dx_dwr_kernel, BOTH_SMEM, done)) != cudaSuccess) return e;
     const int64_t all = resident_pairs(router_dx_dwr_kernel, WR_THREADS, BOTH_SMEM, most_pairs(), resident[2]);
