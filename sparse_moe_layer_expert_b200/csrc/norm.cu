@@ -653,15 +653,14 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const Nor
 
 // dw[c] = sum over the parts, 32 columns per CTA: each of 32 warps takes every
 // 32nd part, then the warps' sums are added in warp order.
-__global__ void __launch_bounds__(1024) norm_dw_join_kernel(const float *__restrict__ part, int n_part, int cols,
-                                                             float *__restrict__ dw) {
+__global__ void __launch_bounds__(1024) norm_dw_join_kernel(const float *part, int n_part, int cols, float *dw) {
   __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
   predecessor_done();
 #pragma unroll 4
-  for (int i = warp; i < n_part; i += 32) s += part[static_cast<int64_t>(i) * cols + c];
+  for (int i = warp; i < n_part; i += 32) s += __ldcg(part + static_cast<int64_t>(i) * cols + c);
   sh[warp][lane] = s;
   __syncthreads();
   if (warp == 0) {

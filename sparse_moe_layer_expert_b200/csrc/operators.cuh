@@ -13,7 +13,9 @@ namespace moe {
 // still runs (dependents_start), and a kernel launched by launch_next waits,
 // behind its own set-up, until its predecessor is complete and its writes are
 // visible (predecessor_done: before any access to memory that another kernel
-// writes or reads).  Worth about 2 us an edge.
+// writes or reads).  What the predecessor writes changes while such a kernel is
+// under way: its pointers are never const __restrict__ (read-only for a kernel's
+// lifetime), and __ldg does not read them.  Worth about 2 us an edge.
 __device__ __forceinline__ void dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void predecessor_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

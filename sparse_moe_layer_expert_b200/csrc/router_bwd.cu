@@ -818,8 +818,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WR_THREADS, 1)
 // dW_r [Nr, cols] from the pieces of each strip, in token order.  CTA (4
 // experts, strip): 64 threads of 4 columns for each expert.  A strip has
 // runs / n_strips + 2 pieces at most; four are read at once.
-__global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__ part, int pairs, int n_strips,
-                                                        int n_stages, int Nr, int cols, float *__restrict__ out) {
+__global__ void __launch_bounds__(256) dwr_join_kernel(const float *part, int pairs, int n_strips, int n_stages,
+                                                        int Nr, int cols, float *out) {
   const int strip = blockIdx.y;
   const int e = blockIdx.x * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
   const int units = n_strips * n_stages;
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(256) dwr_join_kernel(const float *__restrict__
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (i + k < n) v[k] = *reinterpret_cast<const float4 *>(src + (i + k) * 65536ll);
+      if (i + k < n) v[k] = __ldcg(reinterpret_cast<const float4 *>(src + (i + k) * 65536ll));
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i + k < n) {

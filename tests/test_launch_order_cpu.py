@@ -66,3 +66,11 @@ def test_there_are_some():
 @pytest.mark.parametrize("file,kernel", EARLY)
 def test_early_kernels_wait(file, kernel):
     waits_first(SOURCES[file], kernel)
+
+
+@pytest.mark.parametrize("file,kernel", EARLY)
+def test_early_kernels_do_not_read_as_if_read_only(file, kernel):
+    """Their inputs are written while they are already under way."""
+    for name, params, b in waits_first(SOURCES[file], kernel):
+        assert not re.search(r"const [^,]*__restrict__", params), name
+        assert "__ldg(" not in b, name
