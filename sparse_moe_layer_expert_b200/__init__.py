@@ -4,7 +4,9 @@ The layer ("DeepSeek-V3 Technischer Bericht", Methode section 2, and the FP8
 recipe of its Kernideen section) runs in the CUDA kernels of libmoefp8.so
 behind the C ABI in include/moe_fp8.h; this package is its thin Python
 binding.  Importing it raises ImportError when the library has not been built
-(`python sparse_moe_layer_expert_b200/build.py`); there is no fallback.
+(`python sparse_moe_layer_expert_b200/build.py`); there is no fallback.  The
+operators around the layer need its native binding (_native.so, the same
+build) and raise ImportError without it.
 """
 from ._binding import (  # noqa: F401
     EXPORTS, LIB_PATH, MOE_PROFILE_EVENTS, MOE_PROFILE_BWD_EVENTS, MOE_ROUTE_NOALLOC_SCRATCH_BYTES, PROFILE_STAGES,

@@ -19,12 +19,25 @@ LIB_PATH = os.path.join(_HERE, "libmoefp8.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python sparse_moe_layer_expert_b200/build.py`")
 
-NATIVE_PATH = os.path.join(_HERE, "_native.so")
-if not os.path.exists(NATIVE_PATH):
-    raise ImportError(f"{NATIVE_PATH} is missing: build it with `python sparse_moe_layer_expert_b200/build.py`")
-
 lib = C.CDLL(LIB_PATH)
-from . import _native  # noqa: E402
+
+
+class _NoNative:
+    """In _native's place where it is missing or made for another torch: what
+    needs it raises ImportError, everything else works."""
+
+    def __init__(self, why: str):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self.why}: build it with `python sparse_moe_layer_expert_b200/build.py`")
+
+
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
+try:
+    from . import _native
+except ImportError as _e:
+    _native = _NoNative(str(_e) if os.path.exists(NATIVE_PATH) else f"{NATIVE_PATH} is missing")
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = -1
@@ -512,10 +525,11 @@ def _scratch(fn, idx: int, *args) -> torch.Tensor:
 
 # The calls of a decode or training step go through _native (csrc/binding.cpp),
 # which checks their arguments, allocates what is not given and calls the C ABI.
-_native.init(MoeError, *(C.cast(getattr(lib, n), C.c_void_p).value for n in (
-    "fp8_add_rmsnorm_quant_1x128", "add_rmsnorm_backward_workspace_size", "add_rmsnorm_backward",
-    "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_router_backward_workspace_size",
-    "moe_router_backward")))
+if not isinstance(_native, _NoNative):
+    _native.init(MoeError, *(C.cast(getattr(lib, n), C.c_void_p).value for n in (
+        "fp8_add_rmsnorm_quant_1x128", "add_rmsnorm_backward_workspace_size", "add_rmsnorm_backward",
+        "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_router_backward_workspace_size",
+        "moe_router_backward")))
 
 
 def _launch(fn, t, *args):

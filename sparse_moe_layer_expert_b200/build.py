@@ -51,6 +51,8 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Both libraries, what is out of date of them (or all, with force)."""
+    build_native(force)
     if not force and up_to_date():
         return LIB
     objdir = os.path.join(HERE, "_build")
@@ -91,6 +93,5 @@ def build_native(force: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build_native(force="--force" in sys.argv)
     build(force="--force" in sys.argv, verbose="--verbose" in sys.argv)
     print(LIB)
