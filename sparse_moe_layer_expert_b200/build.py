@@ -72,10 +72,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _made_for() -> str:
+    """What a native binding is good for: this Python's and this torch's ABI."""
+    import importlib.metadata
+    import sysconfig
+    return f"made for {sysconfig.get_config_var('SOABI')}, torch {importlib.metadata.version('torch')}."
+
+
+def native_up_to_date() -> bool:
+    if not os.path.exists(NATIVE):
+        return False
+    t = os.path.getmtime(NATIVE)
+    if any(os.path.getmtime(d) > t for d in (os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moe_fp8.h"))):
+        return False
+    with open(NATIVE, "rb") as f:  # the module carries the text (MOE_MADE_FOR)
+        return _made_for().encode() in f.read()
+
+
 def build_native(force: bool = False) -> str:
-    src = os.path.join(CSRC, "binding.cpp")
-    deps = [src, os.path.join(INCLUDE, "moe_fp8.h")]
-    if not force and os.path.exists(NATIVE) and all(os.path.getmtime(d) <= os.path.getmtime(NATIVE) for d in deps):
+    if not force and native_up_to_date():
         return NATIVE
     import sysconfig
 
@@ -84,9 +99,11 @@ def build_native(force: bool = False) -> str:
     lib = os.path.join(t, "lib")
     tmp = NATIVE + f".tmp{os.getpid()}"
     subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    f'-DMOE_MADE_FOR="{_made_for()}"', "-I", INCLUDE,
                     "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
-                    "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), src, "-o", tmp, "-L", lib,
+                    "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                    os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib,
                     "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"], check=True)
     os.replace(tmp, NATIVE)
     return NATIVE

@@ -410,7 +410,11 @@ PyMethodDef methods[] = {def<init, 8>("init"),
                          def<balance_loss, 10>("balance_loss"),
                          def<router_backward, 14>("router_backward"),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// The doc string says which Python and torch the module was built against; build.py looks for it.
+#ifndef MOE_MADE_FOR
+#define MOE_MADE_FOR ""
+#endif
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", MOE_MADE_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

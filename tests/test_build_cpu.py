@@ -37,6 +37,25 @@ def test_one_call_builds_both(build):
     assert len(build.runs) == 1  # up to date
 
 
+def test_binding_is_made_anew_for_another_torch_or_python(build, monkeypatch):
+    import importlib.metadata
+    import sysconfig
+    build.build()
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "9.9.9")
+    build.build()
+    build.build()
+    assert len(build.runs) == 2
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-999")
+    build.build()
+    assert len(build.runs) == 3
+
+
+def test_the_built_binding_says_what_it_is_for():
+    import torch
+    from sparse_moe_layer_expert_b200 import _native
+    assert _native.__doc__ and torch.__version__.split("+")[0] in _native.__doc__
+
+
 CALLS = """
 import sys, torch
 import sparse_moe_layer_expert_b200 as m
