@@ -13,9 +13,9 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <exception>
 #include <initializer_list>
 #include <string>
 
@@ -162,15 +162,14 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n, Py_ssize_t want_n)
     PyErr_Format(PyExc_TypeError, "%zd arguments, wanted %zd", n, want_n);
     return nullptr;
   }
+  // torch's errors become its Python exceptions (torch.OutOfMemoryError and the like)
+  HANDLE_TH_ERRORS
   try {
     return F(a);
   } catch (const Raised &) {
-  } catch (const std::exception &e) {  // torch's own errors, e.g. out of memory
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    return nullptr;
   }
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // stream, x, resid, weight, eps, h, y, q, scales, rstd, pow2
