@@ -532,6 +532,12 @@ if not isinstance(_native, _NoNative):
         "moe_router_backward")))
 
 
+def _cfg_address(where: str, cfg) -> int:
+    if not isinstance(cfg, MoeConfig):
+        _refuse(where, f"cfg is {type(cfg).__name__}, wanted MoeConfig")
+    return C.addressof(cfg)
+
+
 def _launch(fn, t, *args):
     """fn(current stream of t's device, *args) with that device current (the
     library launches on the current device)."""
@@ -591,8 +597,8 @@ def moe_balance_loss(cfg: MoeConfig, logits, idx, seq_offsets, alpha: float = 1e
     if stream is not None:
         with _use_stream(stream, logits):
             return moe_balance_loss(cfg, logits, idx, seq_offsets, alpha, loss, counts, ws, err)
-    return _launch(_native.balance_loss, logits, C.addressof(cfg), logits, idx, seq_offsets, alpha, loss, counts, ws,
-                   err)
+    return _launch(_native.balance_loss, logits, _cfg_address("moe_balance_loss", cfg), logits, idx, seq_offsets, alpha,
+                   loss, counts, ws, err)
 
 
 def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None, balance=None, dlogits=None, dx=None,
@@ -607,8 +613,8 @@ def moe_router_backward(cfg: MoeConfig, logits, idx, x=None, wr=None, dgate=None
         with _use_stream(stream, logits):
             return moe_router_backward(cfg, logits, idx, x, wr, dgate, balance, dlogits, dx, dx_accumulate, dwr, ws,
                                        err)
-    return _launch(_native.router_backward, logits, C.addressof(cfg), logits, idx, x, wr, dgate, balance, dlogits, dx,
-                   dx_accumulate, dwr, ws, err)
+    return _launch(_native.router_backward, logits, _cfg_address("moe_router_backward", cfg), logits, idx, x, wr, dgate,
+                   balance, dlogits, dx, dx_accumulate, dwr, ws, err)
 
 
 def _sequences(where: str, off, idx: int):
