@@ -76,8 +76,7 @@ __global__ void __launch_bounds__(BAL_WARPS * 32, B == 1 ? 4 : 2) balance_pieces
         sum += v[i];
       }
       sum = warp_sum(sum);
-      // all affinities 0 (every logit far below the exponential's range): no share
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = share_scale(sum);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
       if (lane < a.Kr) {

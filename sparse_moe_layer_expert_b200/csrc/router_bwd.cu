@@ -150,11 +150,11 @@ __global__ void __launch_bounds__(256, B == 1 ? 4 : 2) router_dz_kernel(const Dz
         }
         sum = warp_sum(sum);
         fp = warp_sum(fp);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        fp *= inv;
-        const float c = kk * inv;
+        const float inv = share_scale(sum);
+        // the share first: kk inv alone could overflow where the affinities are tiny
+        const float kfp = kk * (fp * inv);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) dz[i] = c * po[i] * (f[i] - fp);
+        for (int i = 0; i < EPL; ++i) dz[i] = po[i] * inv * fmaf(kk, f[i], -kfp);
       }
     }
     if (a.dgate || a.gdot) {

@@ -10,8 +10,8 @@ namespace moe {
 constexpr int EPL = 8;  // experts per lane (N_r <= 256)
 
 // s_{e,t} from the router's logit partials: the K splits are added in split
-// order, then the sigmoid.  Every kernel that needs the affinities computes
-// them here, so they agree bit for bit.
+// order, then the sigmoid; what selects and gates, and what moe_seq_balance_loss
+// adds up, takes them from here.  (sigmoid_pair() is within a step of it.)
 __device__ __forceinline__ float affinity(const float *__restrict__ partial, int n_ks, int64_t T, int Nr,
                                           int64_t t, int e) {
   float z = 0.0f;
@@ -100,12 +100,22 @@ __device__ __forceinline__ float load_logit(const float *__restrict__ partial, i
 }
 
 // s and 1 - s.  For z >= 0, 1 - s = e^-z s (1 - s itself would cancel); below,
-// s < 1/2 and the difference keeps its digits.  The reciprocal is the
-// hardware's (1 ulp), as these feed gradients and sums, not the selection.
+// s < 1/2 and the difference keeps its digits.  The reciprocal is the hardware's,
+// one FP32 step off at most where affinity()'s is half of one: it feeds gradients
+// and sums of shares, not the selection (the IEEE one: 30.9 us a loss with its
+// gradient at 16384 x 256, this one 27.2).  1 + q is taken 2^-24 times, so that
+// the subnormal s of -88.7 < z < -87.3 is not flushed.
 __device__ __forceinline__ void sigmoid_pair(float z, float &s, float &om) {
   const float q = expf(-z);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + q));  // q = inf gives 0
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(q, 0x1p-24f, 0x1p-24f)));  // q = inf gives 0
+  s *= 0x1p-24f;
   om = z >= 0.0f ? q * s : 1.0f - s;
+}
+
+// 1 / sum of a token's affinities (0 if all of them are 0: every logit far below
+// the exponential's range, and no share); finite for the smallest sum too, 2^-128.
+__device__ __forceinline__ float share_scale(float sum) {
+  return sum > 0.0f ? fminf(1.0f / sum, 3.402823466e38f) : 0.0f;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
