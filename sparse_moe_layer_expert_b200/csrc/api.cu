@@ -1210,7 +1210,7 @@ int fp8_add_rmsnorm_quant_1x128(const void *x, int64_t ld_x, const void *resid, 
 
 size_t add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows < 0 || rows > INT32_MAX || cols <= 0 || cols % 128 || cols > kMaxK) return 0;
-  const size_t n = static_cast<size_t>(moe::norm_bwd_parts(rows, static_cast<int>(cols))) * cols * 4;
+  const size_t n = static_cast<size_t>(moe::norm_bwd_parts(rows)) * cols * 4;
   return n < 256 ? 256 : n;
 }
 

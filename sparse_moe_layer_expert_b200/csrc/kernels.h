@@ -229,8 +229,8 @@ cudaError_t launch_wait_selftest(int32_t *err, uint64_t limit_ns, cudaStream_t s
 cudaError_t launch_add_rmsnorm_quant(const void *x, int64_t ld_x, const void *resid, int64_t ld_r, bool f32,
                                      const float *w, float eps, int64_t rows, int cols, void *h, void *y, uint8_t *q,
                                      float *s, float *rstd, bool pow2, cudaStream_t st);
-// part: [norm_bwd_parts(rows, cols), cols] floats (when dw is given)
-int norm_bwd_parts(int64_t rows, int cols);
+// part: [norm_bwd_parts(rows), cols] floats (when dw is given)
+int norm_bwd_parts(int64_t rows);
 cudaError_t launch_add_rmsnorm_bwd(const void *dy, bool dy_f32, const void *h, const void *dres, bool f32,
                                    const float *w, const float *rstd, int64_t rows, int cols, void *dx, bool dx_f32,
                                    float *dw, float *part, cudaStream_t st);

@@ -723,10 +723,13 @@ template <typename TS, int CH, bool POW2>
 cudaError_t launch_norm_rows(const NormFwd &p, cudaStream_t st) {
   const dim3 b = norm_block(p.cols, CH);
   const unsigned grid = static_cast<unsigned>((p.rows + b.y - 1) / b.y);
-  if (b.x * b.y <= 256)
-    add_rmsnorm_quant_kernel<TS, CH, POW2, 256><<<grid, b, 0, st>>>(p);
-  else
-    add_rmsnorm_quant_kernel<TS, CH, POW2, 1024><<<grid, b, 0, st>>>(p);
+  if constexpr (CH == 1) {  // (rows of several chunks a thread have more than 256 threads)
+    if (b.x * b.y <= 256) {
+      add_rmsnorm_quant_kernel<TS, CH, POW2, 256><<<grid, b, 0, st>>>(p);
+      return cudaGetLastError();
+    }
+  }
+  add_rmsnorm_quant_kernel<TS, CH, POW2, 1024><<<grid, b, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -803,7 +806,7 @@ cudaError_t launch_add_rmsnorm_quant(const void *x, int64_t ld_x, const void *re
 }
 
 // An upper bound on the CTAs of either backward kernel.
-int norm_bwd_parts(int64_t rows, int) {
+int norm_bwd_parts(int64_t rows) {
   const int64_t most = kMaxCtas * static_cast<int64_t>(moe_host::sm_count());
   return static_cast<int>(rows < most ? rows : most);
 }
