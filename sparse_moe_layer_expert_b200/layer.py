@@ -101,18 +101,18 @@ class MoeLayer:
     def workspace(self, T: int) -> torch.Tensor:
         ws = self._ws.get(T)
         if ws is None:
-            n = max(B.moe_workspace_size(self.cfg, T), 256)
-            g = self.guard_bytes
-            if g:
-                assert g % 256 == 0
-                buf = torch.full((n + 2 * g,), self.GUARD_BYTE, dtype=torch.uint8, device=self.device)
-                ws = buf[g:g + n]
-                self._guarded = getattr(self, "_guarded", [])
-                self._guarded.append((buf, g, n))
-            else:
-                ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            self._ws[T] = ws
+            ws = self._ws[T] = self._scratch(B.moe_workspace_size(self.cfg, T))
         return ws
+
+    def _scratch(self, nbytes: int) -> torch.Tensor:
+        n, g = max(int(nbytes), 256), self.guard_bytes
+        if not g:
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        assert g % 256 == 0
+        buf = torch.full((n + 2 * g,), self.GUARD_BYTE, dtype=torch.uint8, device=self.device)
+        self._guarded = getattr(self, "_guarded", [])
+        self._guarded.append((buf, g, n))
+        return buf[g:g + n]
 
     # What a call allocates belongs to the stream it runs on; what it finds is
     # made known to the allocator as used there too, so that neither is given
@@ -204,9 +204,7 @@ class MoeLayer:
             bws = self._bws = {}
         ws = bws.get(T)
         if ws is None:
-            ws = torch.empty(max(int(B.lib.moe_backward_workspace_size(B.ctypes_cfg(self.cfg), T)), 256),
-                             dtype=torch.uint8, device=self.device)
-            bws[T] = ws
+            ws = bws[T] = self._scratch(B.lib.moe_backward_workspace_size(B.ctypes_cfg(self.cfg), T))
         return ws
 
     # ---------------------------------------------- the block: norm + layer
@@ -260,9 +258,7 @@ class MoeLayer:
             bws = self._bbws = {}
         ws = bws.get(T)
         if ws is None:
-            ws = torch.empty(max(int(B.lib.moe_block_backward_workspace_size(B.ctypes_cfg(self.cfg), T)), 256),
-                             dtype=torch.uint8, device=self.device)
-            bws[T] = ws
+            ws = bws[T] = self._scratch(B.lib.moe_block_backward_workspace_size(B.ctypes_cfg(self.cfg), T))
         return ws
 
     def check(self, stream=None) -> None:
