@@ -567,7 +567,8 @@ MOE_API int moe_router_splits(const moe_config *cfg, int64_t T);
  *   ws_dev      moe_balance_loss_workspace_size() bytes, 256-byte aligned
  *   err_flag_dev gets MOE_DEVERR_BAD_INDEX for an expert index out of range
  *               (not counted) and for offsets that are not as above (such a
- *               sequence is read as empty)
+ *               sequence is read as empty; the other sequences' outputs are
+ *               not to be used then either)
  * n_seq == 0 enqueues nothing.  The additions' order is fixed: every run gives
  * the same bits. */
 MOE_API size_t moe_balance_loss_workspace_size(const moe_config *cfg, int64_t T, int64_t n_seq);
