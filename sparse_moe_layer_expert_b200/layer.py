@@ -44,7 +44,8 @@ class MoeLayer:
         B.fp8_quant_128x128(w2_bf16.contiguous(), q=self.w2[e], scales=self.s2[e], stream=stream, pow2=pow2)
         wt = self._wt
         if wt is not None:
-            one = slice(e, e + 1)
+            first = range(self.E)[e]  # e may count from the end
+            one = slice(first, first + 1)
             B.moe_transpose_weights(B.config(self.cfg.hidden, self.cfg.inter, 1, 1, 0),
                                     {k: t if k == "wr" else t[one] for k, t in self.weights().items()},
                                     out={k: t[one] for k, t in wt.items()}, stream=stream)
@@ -87,6 +88,10 @@ class MoeLayer:
         other._ws = {}
         other._copies = self._copies
         return other
+
+    def __getstate__(self) -> dict:
+        # a copy of the layer makes transposed weights of its own
+        return dict(self.__dict__, _copies={})
 
     def weights(self) -> dict:
         return dict(w13=self.w13, s13=self.s13, w2=self.w2, s2=self.s2, wr=self.wr)

@@ -1,4 +1,6 @@
 """The block's backward after its weights have changed."""
+import copy
+
 import pytest
 import torch
 
@@ -85,3 +87,20 @@ def test_other_tensors_in_the_weights_places(m):
         setattr(layer, k, getattr(other, k))
     same(run(layer, *args), want)
     same(run(sib, *args), mine)
+
+
+def test_expert_counted_from_the_end_and_a_copied_layer(m):
+    T = 40
+    cfg, layer, x, resid, w, dout = problem(m, T, 36)
+    args = (x, resid, w, dout)
+    run(layer, *args)
+    twin = copy.deepcopy(layer)
+    before = run(layer, *args)
+    w13, w2 = (t.cuda() for t in S.gen_expert(3, cfg["H"], cfg["I"], 950))
+    fresh = problem(m, T, 36)[1]
+    fresh.set_expert(cfg["Nr"], w13, w2)
+    layer.set_expert(-1, w13, w2)  # the shared expert
+    same(run(layer, *args), run(fresh, *args))
+    same(run(twin, *args), before)
+    with pytest.raises(IndexError):
+        layer.set_expert(layer.E, w13, w2)

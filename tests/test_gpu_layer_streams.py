@@ -61,7 +61,7 @@ def test_transposed_weights_made_on_another_stream(m):
         _, s2 = layer.block_forward(x2, r2, w, EPS)
     torch.cuda.synchronize()
     with torch.cuda.stream(a):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(1_000_000_000)
         g1 = layer.block_backward(s1, d1)
     with torch.cuda.stream(b):
         g2 = layer.block_backward(s2, d2)
@@ -81,7 +81,7 @@ def test_layer_freed_while_another_stream_works(m):
     torch.cuda.synchronize()
     torch.cuda._sleep(1)
     with torch.cuda.stream(st):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(1_000_000_000)
         got = layer.block_forward(x, resid, w, EPS)[0]
     layer._ws.clear()
     layer._guarded = []
